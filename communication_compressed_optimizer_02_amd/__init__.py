@@ -9,6 +9,9 @@ from .binding import (OBA_BF16, OBA_F16, OBA_F32, Layout, ObaError, Plateau, Sta
                       decompress_update_listed,
                       adam_warmup_step_vnorm, compress, compress_deferred_local,
                       compress_deferred, decompress_update, deferred_errors, freeze_variance,
+                      act8_buffers, act8_decode, act8_encode, layer_norm, layer_norm_backward,
+                      layer_norm_backward_workspace, linear, linear_input_grad,
+                      linear_weight_grad, linear_weight_grad_workspace, linear_workspace,
                       server_momentum, server_reduce_recompress,
                       server_reduce_recompress_deferred, step_small, timing_enable, timing_read, timing_reset, validate)
 
@@ -21,4 +24,7 @@ __all__ = [
     "server_momentum", "server_reduce_recompress", "server_reduce_recompress_deferred",
     "step_small", "timing_enable",
     "timing_read", "timing_reset", "validate",
+    "act8_buffers", "act8_decode", "act8_encode", "layer_norm", "layer_norm_backward",
+    "layer_norm_backward_workspace", "linear", "linear_input_grad", "linear_weight_grad",
+    "linear_weight_grad_workspace", "linear_workspace",
 ]

@@ -11,6 +11,11 @@ Buffers (all CUDA tensors on the layout's device, C-contiguous):
   x, m, v, denom, eps  [d] float32
   wbits  [n][W]  int64 (packed 64-bit words)   sbits [W] int64
   wscale [n][n_wseg] float32                   sscale [n_sseg] float32
+
+The layer calls (act8_*, layer_norm*, linear*) take matrices as 2-D tensors
+with rows of a stride that is a multiple of 8 elements (columns adjacent),
+and activations kept in 8 bits as the pair (q, e) of act8_buffers().  Their
+tensors must be on the current device.
 """
 from __future__ import annotations
 
@@ -59,6 +64,20 @@ SIGNATURES = {
                                             _P]),
     "oba_decompress_update_listed": (_I, [_P, _P, _P, _P, _P, _P, _D, _P]),
     "oba_step_small": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _D, _D, _P]),
+    "oba_act8_encode": (_I, [_I64, _I64, _P, _I64, _I, _P, _P, _P]),
+    "oba_act8_decode": (_I, [_I64, _I64, _P, _P, _P, _I64, _I, _P]),
+    "oba_layer_norm": (_I, [_I64, _I64, _P, _I64, _I, _P, _P, _D, _P, _I64, _P, _P, _P, _P, _P]),
+    "oba_layer_norm_backward_workspace_bytes": (_SZ, [_I32, _I64, _I64]),
+    "oba_layer_norm_backward": (_I, [_I32, _I64, _I64, _P, _I64, _I, _P, _I64, _P, _P, _P, _P, _P,
+                                     _P, _I64, _P, _I64, _P, _P, _I, _I64, _P, _SZ, _P]),
+    "oba_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "oba_linear": (_I, [_I64, _I64, _I64, _P, _I64, _P, _I64, _I, _P, _I, _P, _I64, _P, _I64, _P,
+                        _P, _P, _SZ, _P]),
+    "oba_linear_input_grad": (_I, [_I64, _I64, _I64, _P, _I64, _P, _I64, _I, _I, _P, _P, _P, _I64,
+                                   _P, _I64, _P, _SZ, _P]),
+    "oba_linear_weight_grad_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64]),
+    "oba_linear_weight_grad": (_I, [_I32, _I64, _I64, _I64, _P, _I64, _I, _P, _P, _P, _P, _I, _I64,
+                                    _P, _SZ, _P]),
     "oba_timing_enable": (_I, [_I, _I32]),
     "oba_timing_read": (_I, [ctypes.c_char_p, ctypes.POINTER(_D), ctypes.POINTER(_I64)]),
     "oba_timing_reset": (_I, []),
@@ -542,6 +561,264 @@ def step_small(L: Layout, g, m, c, wbits, wscale, a, sbits, sscale, denom, m_out
         _ptr(m_out, "m_out", f32, (L.d,)) if m_out is not None else P(None),
         _ptr(x, "x", f32, (L.d,)), beta1, lr, _stream(stream))
     _check(rc, "oba_step_small")
+
+
+# ---- layers: norm, linear, activations kept in 8 bits -------------------------
+
+ACT8_GROUP = 32
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3}
+_TYPES = None  # torch dtype -> OBA code (filled at the first call: torch is imported late)
+
+
+def _types():
+    global _TYPES
+    if _TYPES is None:
+        import torch
+
+        _TYPES = {torch.float32: OBA_F32, torch.float16: OBA_F16, torch.bfloat16: OBA_BF16}
+    return _TYPES
+
+
+class _Call:
+    """Argument checks of one layer call: every tensor on the current device."""
+
+    __slots__ = ("torch", "dev")
+
+    def __init__(self):
+        import torch
+
+        self.torch = torch
+        self.dev = torch.cuda.current_device()
+
+    def stream(self, stream):
+        return self.torch.cuda.current_stream(self.dev).cuda_stream if stream is None \
+            else stream.cuda_stream
+
+    def _on(self, t, name):
+        if not isinstance(t, self.torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name}: expected a CUDA tensor")
+        if t.get_device() != self.dev:
+            raise ValueError(f"{name}: on {t.device}, the current device is cuda:{self.dev}")
+
+    def rows(self, t, name, rows=None, cols=None, dtype=None):
+        """(pointer, row stride) of a matrix; the shape and the type are
+        checked where they are given."""
+        self._on(t, name)
+        if t.dim() != 2:
+            raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
+        r, c = t.shape
+        if (rows is not None and r != rows) or (cols is not None and c != cols):
+            raise ValueError(f"{name}: shape {tuple(t.shape)} != {(rows, cols)}")
+        if t.dtype not in _types() or (dtype is not None and t.dtype != dtype):
+            raise TypeError(f"{name}: dtype {t.dtype}" +
+                            (f" != {dtype}" if dtype is not None else " not supported"))
+        ld, one = t.stride()
+        wide = (c + 7) // 8 * 8
+        if r <= 1:  # a single row has no stride
+            ld = wide
+        if (one != 1 and c > 1) or ld % 8 or ld < c:
+            raise ValueError(f"{name}: columns must be adjacent and rows a multiple of 8 elements "
+                             f"apart, got strides {t.stride()} for {c} columns")
+        if wide != c and r and (t.storage_offset() + (r - 1) * ld + wide) * t.element_size() > \
+                t.untyped_storage().nbytes():
+            raise ValueError(f"{name}: the last row's memory must reach {wide} columns "
+                             "(columns rounded up to 8)")
+        return t.data_ptr(), ld
+
+    def vec(self, t, name, dtype, size):
+        self._on(t, name)
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
+        if t.numel() != size or not t.is_contiguous():
+            raise ValueError(f"{name}: expected {size} contiguous elements, got {tuple(t.shape)}")
+        return t.data_ptr()
+
+    def kept(self, q, e, rows, cols):
+        """Pointers of an 8-bit pair, or of none."""
+        if q is None and e is None:
+            return None, None
+        if q is None or e is None:
+            raise ValueError("q and e: both or neither")
+        g = (cols + ACT8_GROUP - 1) // ACT8_GROUP
+        for t, name, dt, shape in ((q, "q", self.torch.int8, (rows, g * ACT8_GROUP)),
+                                   (e, "e", self.torch.uint8, (rows, g))):
+            self._on(t, name)
+            if t.dtype != dt:
+                raise TypeError(f"{name}: dtype {t.dtype} != {dt}")
+            if t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}, contiguous")
+        return q.data_ptr(), e.data_ptr()
+
+    def grads(self, g, n, *places):
+        """(type, stride, pointers) of parameter tensors' places (offset or
+        None, length) in the gradient rows g [n][ld]."""
+        self._on(g, "g")
+        if g.dtype not in _types():
+            raise TypeError(f"g: dtype {g.dtype} not supported")
+        if g.dim() != 2 or g.shape[0] != n or not g.is_contiguous():
+            raise ValueError(f"g: expected {n} contiguous rows, got {tuple(g.shape)}")
+        ld, size, base, out = g.shape[1], g.element_size(), g.data_ptr(), []
+        taken = []
+        for at, length in places:
+            if at is None:
+                out.append(None)
+                continue
+            if at < 0 or at + length > ld:
+                raise ValueError(f"g: no {length} elements at {at} in rows of {ld}")
+            if any(at < b and a < at + length for a, b in taken):
+                raise ValueError("g: two gradients overlap")
+            taken.append((at, at + length))
+            out.append(base + at * size)
+        return _types()[g.dtype], ld, out
+
+    def ws(self, ws):
+        if ws is None:
+            return None, 0
+        self._on(ws, "ws")
+        if not ws.is_contiguous():
+            raise ValueError("ws: must be contiguous")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _workspace(nbytes):
+    import torch
+
+    return torch.empty(max(16, nbytes), dtype=torch.uint8, device="cuda")
+
+
+def act8_buffers(rows, cols):
+    """(q, e): buffers for a [rows][cols] matrix kept in 8 bits."""
+    import torch
+
+    g = (cols + ACT8_GROUP - 1) // ACT8_GROUP
+    return (torch.empty((rows, g * ACT8_GROUP), dtype=torch.int8, device="cuda"),
+            torch.empty((rows, g), dtype=torch.uint8, device="cuda"))
+
+
+def act8_encode(x, q, e, stream=None):
+    """x [rows][cols] (float32, float16 or bfloat16) to 8 bits."""
+    c = _Call()
+    xp, ldx = c.rows(x, "x")
+    qp, ep = c.kept(q, e, *x.shape)
+    _check(lib().oba_act8_encode(*x.shape, xp, ldx, _types()[x.dtype], qp, ep, c.stream(stream)),
+           "oba_act8_encode")
+
+
+def act8_decode(q, e, x, stream=None):
+    """The values that (q, e) stand for, written to x."""
+    c = _Call()
+    xp, ldx = c.rows(x, "x")
+    qp, ep = c.kept(q, e, *x.shape)
+    _check(lib().oba_act8_decode(*x.shape, qp, ep, xp, ldx, _types()[x.dtype], c.stream(stream)),
+           "oba_act8_decode")
+
+
+def layer_norm(x, gamma, beta, eta, y, mean, rstd, q=None, e=None, stream=None):
+    """y = xhat * gamma + beta; mean and rstd [rows] float32 are written; with
+    (q, e) xhat is kept in 8 bits."""
+    c = _Call()
+    f32 = c.torch.float32
+    rows, cols = x.shape
+    xp, ldx = c.rows(x, "x")
+    yp, ldy = c.rows(y, "y", rows, cols, x.dtype)
+    qp, ep = c.kept(q, e, rows, cols)
+    _check(lib().oba_layer_norm(rows, cols, xp, ldx, _types()[x.dtype],
+                                c.vec(gamma, "gamma", f32, cols), c.vec(beta, "beta", f32, cols),
+                                eta, yp, ldy, c.vec(mean, "mean", f32, rows),
+                                c.vec(rstd, "rstd", f32, rows), qp, ep, c.stream(stream)),
+           "oba_layer_norm")
+
+
+def layer_norm_backward_workspace(n, rows, cols):
+    """A workspace for layer_norm_backward of n workers with `rows` rows each."""
+    return _workspace(lib().oba_layer_norm_backward_workspace_bytes(n, rows, cols))
+
+
+def layer_norm_backward(n, dy, gamma, rstd, dx, g, at_gamma, at_beta, ws, x=None, mean=None,
+                        q=None, e=None, add=None, stream=None):
+    """dx, and every worker's gradients of gamma and beta at these offsets of
+    its row of g [n][ld].  The normalised rows come from (x, mean) or from
+    (q, e); add: the gradient that goes round the layer, or None."""
+    c = _Call()
+    f32 = c.torch.float32
+    dyp, lddy = c.rows(dy, "dy")
+    total, cols = dy.shape
+    if n < 1 or total % n:
+        raise ValueError(f"dy: {total} rows are not {n} equal parts")
+    xp, ldx = c.rows(x, "x", total, cols, dy.dtype) if x is not None else (None, 0)
+    ap, lda = c.rows(add, "add", total, cols, dy.dtype) if add is not None else (None, 0)
+    dxp, lddx = c.rows(dx, "dx", total, cols, dy.dtype)
+    qp, ep = c.kept(q, e, total, cols)
+    gt, ldg, (gp, bp) = c.grads(g, n, (at_gamma, cols), (at_beta, cols))
+    wp, wb = c.ws(ws)
+    _check(lib().oba_layer_norm_backward(
+        n, total // n, cols, dyp, lddy, _types()[dy.dtype], xp, ldx,
+        c.vec(mean, "mean", f32, total) if mean is not None else None, qp, ep,
+        c.vec(rstd, "rstd", f32, total), c.vec(gamma, "gamma", f32, cols), ap, lda, dxp, lddx,
+        gp, bp, gt, ldg, wp, wb, c.stream(stream)), "oba_layer_norm_backward")
+
+
+def linear_workspace(rows, n_in, n_out):
+    """A workspace for linear and linear_input_grad of these sizes."""
+    return _workspace(lib().oba_linear_workspace_bytes(rows, n_in, n_out))
+
+
+def linear(x, w, y, ws, bias=None, act="none", residual=None, q=None, e=None, stream=None):
+    """y = act(x w^T + bias) + residual (float16 or bfloat16, bias float32);
+    with (q, e) the pre-activation is kept in 8 bits."""
+    c = _Call()
+    xp, ldx = c.rows(x, "x")
+    rows, n_in = x.shape
+    wp, ldw = c.rows(w, "w", None, n_in, x.dtype)
+    n_out = w.shape[0]
+    yp, ldy = c.rows(y, "y", rows, n_out, x.dtype)
+    rp, ldr = c.rows(residual, "residual", rows, n_out, x.dtype) if residual is not None \
+        else (None, 0)
+    qp, ep = c.kept(q, e, rows, n_out)
+    sp, sb = c.ws(ws)
+    _check(lib().oba_linear(
+        rows, n_in, n_out, xp, ldx, wp, ldw, _types()[x.dtype],
+        c.vec(bias, "bias", c.torch.float32, n_out) if bias is not None else None, ACTS[act],
+        rp, ldr, yp, ldy, qp, ep, sp, sb, c.stream(stream)), "oba_linear")
+
+
+def linear_input_grad(dy, w, dx, ws, act="none", q=None, e=None, add=None, stream=None):
+    """dx = (dy w) * act'(p) + add, p the pre-activation kept in (q, e)."""
+    c = _Call()
+    dyp, lddy = c.rows(dy, "dy")
+    rows, n_out = dy.shape
+    wp, ldw = c.rows(w, "w", n_out, None, dy.dtype)
+    n_in = w.shape[1]
+    dxp, lddx = c.rows(dx, "dx", rows, n_in, dy.dtype)
+    ap, lda = c.rows(add, "add", rows, n_in, dy.dtype) if add is not None else (None, 0)
+    qp, ep = c.kept(q, e, rows, n_in)
+    sp, sb = c.ws(ws)
+    _check(lib().oba_linear_input_grad(
+        rows, n_in, n_out, dyp, lddy, wp, ldw, _types()[dy.dtype], ACTS[act], qp, ep, ap, lda,
+        dxp, lddx, sp, sb, c.stream(stream)), "oba_linear_input_grad")
+
+
+def linear_weight_grad_workspace(n, rows, n_in, n_out):
+    """A workspace for linear_weight_grad of n workers with `rows` rows each."""
+    return _workspace(lib().oba_linear_weight_grad_workspace_bytes(n, rows, n_in, n_out))
+
+
+def linear_weight_grad(n, dy, q, e, g, n_in, at_w, at_bias, ws, stream=None):
+    """Every worker's dy^T x ([n_out][n_in]) and column sums of dy at these
+    offsets of its row of g [n][ld] (at_bias None: no bias); x kept in (q, e)."""
+    c = _Call()
+    dyp, lddy = c.rows(dy, "dy")
+    total, n_out = dy.shape
+    if n < 1 or total % n:
+        raise ValueError(f"dy: {total} rows are not {n} equal parts")
+    if q is None:
+        raise ValueError("q, e: the layer's input kept in 8 bits is needed")
+    qp, ep = c.kept(q, e, total, n_in)
+    gt, ldg, (gp, bp) = c.grads(g, n, (at_w, n_in * n_out), (at_bias, n_out))
+    sp, sb = c.ws(ws)
+    _check(lib().oba_linear_weight_grad(
+        n, total // n, n_in, n_out, dyp, lddy, _types()[dy.dtype], qp, ep, gp, bp, gt, ldg, sp,
+        sb, c.stream(stream)), "oba_linear_weight_grad")
 
 
 def timing_enable(on=True, capacity=4096):

@@ -36,7 +36,7 @@ HIP_FLAGS = [
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra"]
 # one translation unit per pass, plus the C ABI
 HIP_SOURCES = ("warmup.hip", "compress.hip", "scales.hip", "server.hip", "update.hip",
-               "small.hip", "api.hip")
+               "small.hip", "act8.hip", "norm.hip", "linear.hip", "layer_api.hip", "api.hip")
 
 
 def hipcc() -> str:

@@ -15,6 +15,7 @@
 #include <utility>
 #include <vector>
 
+#include "abi.hpp"
 #include "kernels.hpp"
 #include "layout.hpp"
 #include "oba.h"
@@ -1055,3 +1056,7 @@ int oba_timing_reset(void) {
 }
 
 }  // extern "C"
+
+int oba::abi_launch(const char* name, hipStream_t st, void (*fn)(void*), void* ctx) {
+  return launch(name, st, [&] { fn(ctx); });
+}

@@ -1,0 +1,574 @@
+// linear.hip -- the matrix products of a linear layer on the matrix cores
+// (gfx950), with everything that touches their result in the epilogue.
+//
+//   forward       y[t][f]  = act(sum_k x[t][k] w[f][k] + bias[f]) + residual[t][f]
+//   input grad    dx[t][i] = (sum_o dy[t][o] w[o][i]) act'(p[t][i]) + add[t][i]
+//   weight grad   dw[o][i] = sum_t dy[t][o] x[t][i], db[o] = sum_t dy[t][o]
+//                 (one product per worker, x and p kept in 8 bits)
+//
+// All three are C[r][c] = sum_k B(r, k) A(c, k).  The c side is the "A"
+// operand of v_mfma_f32_16x16x32, so that a lane's four results are four
+// consecutive columns of one row: 8-byte stores, and a group of 32 columns
+// for the 8-bit form is two neighbouring tiles of one wave.  What differs is
+// how an operand lies in memory:
+//   kKRow   [r][k], k contiguous: kept so in LDS and read 16 bytes per lane
+//   kKCol   [k][r], r contiguous: kept so in LDS and transposed by the
+//           ds_read_b64_tr_b16 instruction while it is read
+//   kKept   as kKCol with 8-bit elements, decoded to 16 bits (exactly) on the
+//           way to LDS
+// Sums are binary32 in the accumulators, in increasing k; a product of few
+// tiles is split over k, its binary32 sums joined in split order.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "layer.hpp"
+#include "layer_kernels.hpp"
+
+namespace oba {
+
+namespace {
+
+enum Src { kKRow, kKCol, kKept };
+
+constexpr int kBK = 64;  // the step along k: one 128-byte line of a kKRow operand's row
+
+// ---- the matrix instruction ----------------------------------------------------
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ lf4 mfma(lu4 a, lu4 b, lf4 c, const _Float16*) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a),
+                                                __builtin_bit_cast(h8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ lf4 mfma(lu4 a, lu4 b, lf4 c, const __bf16*) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a),
+                                                 __builtin_bit_cast(b8, b), c, 0, 0, 0);
+}
+
+// ---- LDS layouts -----------------------------------------------------------------
+// kKRow: [R][kBK], 128 bytes a row, the 16-byte pieces of a row permuted by
+// the row's low bits: the 16 rows that a fragment read touches at one k fall
+// on all banks.  kKCol: [kBK][R], the 32-byte blocks of a row permuted by
+// bits of k: a transposing read touches the 16 values of k that differ in
+// bits 0-1 and 3-4, 32 bytes of each.
+__device__ __forceinline__ uint32_t krow_at(uint32_t row, uint32_t piece) {
+  return row * 128u + ((piece ^ (row & 7u)) << 4);
+}
+template <int R>
+__device__ __forceinline__ uint32_t kcol_at(uint32_t k, uint32_t block) {
+  const uint32_t f = (k & 3u) | ((k >> 3) & 3u) << 2;
+  return k * (R * 2u) + (((block ^ f) & (R / 16 - 1)) << 5);
+}
+
+// One thread's share of an operand's tile: its pieces of 8 elements on the
+// way from memory to LDS.  `off` are element offsets from the tile's origin,
+// rows past the operand's end read its last row (results there are not
+// stored).
+template <typename T, int SRC, int R, int NT>
+struct Stage {
+  static constexpr int P = R * (kBK / 8) / NT;
+  lu4 reg[P];
+  uint32_t off[P], eoff[P];
+
+  // r0: first row of the tile, of `rows`; ld, eld: strides in elements
+  __device__ __forceinline__ void init(int32_t r0, int32_t rows, uint32_t ld, uint32_t eld) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const uint32_t i = p * NT + threadIdx.x;
+      if constexpr (SRC == kKRow) {
+        const uint32_t r = i / (kBK / 8), c = i % (kBK / 8);
+        off[p] = min(r, (uint32_t)(rows - 1 - r0)) * ld + c * 8;
+      } else {
+        const uint32_t k = i / (R / 8), c = i % (R / 8);
+        const uint32_t col = min(c * 8, (uint32_t)(rows - 1 - r0) & ~7u);
+        off[p] = k * ld + col;
+        if constexpr (SRC == kKept) eoff[p] = k * eld + col / kAct8Group;
+      }
+    }
+  }
+
+  // left: elements along k from this step to the end of the sum; a step of
+  // fewer than kBK reads nothing past the end and gives zeros there
+  template <bool TAIL>
+  __device__ __forceinline__ void load(const void* __restrict__ base,
+                                       const uint8_t* __restrict__ ebase, int32_t left,
+                                       uint32_t ld, uint32_t eld) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const uint32_t i = p * NT + threadIdx.x;
+      const int32_t k = SRC == kKRow ? (int32_t)(i % (kBK / 8)) * 8 : (int32_t)(i / (R / 8));
+      if (TAIL && k >= left) {
+        reg[p] = lu4{0u, 0u, 0u, 0u};
+        continue;
+      }
+      if constexpr (SRC == kKept) {
+        const lu2 q = *reinterpret_cast<const lu2*>(static_cast<const uint8_t*>(base) + off[p]);
+        reg[p] = lu4{q[0], q[1], (uint32_t)ebase[eoff[p]], 0u};
+      } else {
+        reg[p] = *reinterpret_cast<const lu4*>(static_cast<const T*>(base) + off[p]);
+        if (TAIL && SRC == kKRow && k + 8 > left) {
+          for (int j = 0; j < 4; ++j)
+            reg[p][j] &= (k + 2 * j < left ? 0xFFFFu : 0u) |
+                         (k + 2 * j + 1 < left ? 0xFFFF0000u : 0u);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void store(char* __restrict__ lds) const {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const uint32_t i = p * NT + threadIdx.x;
+      lu4 u = reg[p];
+      if constexpr (SRC == kKept) {
+        // an integer of at most 7 bits times a power of two: exact in T but
+        // for binary16's range, which rows encoded from binary16 do not leave
+        const float s = step_of(reg[p][2]);
+        float v[8];
+        for (int j = 0; j < 8; ++j) v[j] = dequant(reg[p][j / 4], j % 4, s);
+        u = pack(v, (const T*)nullptr);
+      }
+      if constexpr (SRC == kKRow) {
+        *reinterpret_cast<lu4*>(lds + krow_at(i / (kBK / 8), i % (kBK / 8))) = u;
+      } else {
+        const uint32_t c = i % (R / 8);
+        *reinterpret_cast<lu4*>(lds + kcol_at<R>(i / (R / 8), c / 2) + (c & 1) * 16) = u;
+      }
+    }
+  }
+};
+
+// The fragment of 16 rows from `row` at k = 32 * ks: lane l holds row l % 16,
+// k = 8 * (l / 16) .. +7.
+template <int SRC, int R>
+__device__ __forceinline__ lu4 fragment(const char* lds, uint32_t row, uint32_t ks) {
+  const uint32_t l = threadIdx.x & 63;
+  if constexpr (SRC == kKRow) {
+    return *reinterpret_cast<const lu4*>(lds + krow_at(row + (l & 15), ks * 4 + (l >> 4)));
+  } else {
+    // the transposing read gives lane j of 16 the j-th column of a 4 x 16
+    // block whose row i lies in lanes 4i .. 4i+3
+    const uint32_t k = ks * 32 + (l >> 4) * 8 + ((l & 15) >> 2);
+    typedef __attribute__((address_space(3))) s4* lp;
+    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lp)(lds + kcol_at<R>(k, row >> 4) + (l & 3) * 8));
+    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lp)(lds + kcol_at<R>(k + 4, row >> 4) + (l & 3) * 8));
+    const lu2 a = __builtin_bit_cast(lu2, lo), b = __builtin_bit_cast(lu2, hi);
+    return lu4{a[0], a[1], b[0], b[1]};
+  }
+}
+
+// ---- epilogues ---------------------------------------------------------------------
+// Eight results of row r from column c (c % 8 == 0).  n: columns from c to the
+// last (may be more than 8, or none).  Rows of 16-bit operands hold memory up
+// to a multiple of 8 columns.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    *reinterpret_cast<lu4*>(p) = pack(v, (const T*)nullptr);
+  } else {
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = (T)v[j];
+  }
+}
+
+// The forward result from the product, the input gradient from the product:
+// bias, 8-bit pre-activation kept or used, activation or its derivative,
+// residual, one rounding.  Four neighbouring lanes hold a group of 32 columns.
+template <typename T, LinearKind KIND>
+__device__ __forceinline__ void finish(const Linear& a, bool in_rows, int64_t r, int32_t c,
+                                       float (&v)[8]) {
+  const int n = a.cols - c;
+  const int32_t groups = (a.cols + kAct8Group - 1) / kAct8Group;
+  const int64_t g = r * groups + c / kAct8Group;
+  if constexpr (KIND == LinearKind::kForward) {
+    if (a.bias)
+      for (int j = 0; j < 8; ++j) v[j] += j < n ? a.bias[c + j] : 0.0f;
+    if (a.q) {  // columns past the last are kept as 0
+      uint32_t top = 0;
+      float w[8];
+      for (int j = 0; j < 8; ++j) {
+        w[j] = j < n ? v[j] : 0.0f;
+        top = max(top, magnitude(w[j]));
+      }
+      top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+      const uint32_t ex = group_exp(top);
+      const float inv = inv_step_of(ex);
+      if (in_rows && c / kAct8Group < groups) {
+        *reinterpret_cast<lu2*>(a.q + g * kAct8Group + c % kAct8Group) =
+            lu2{quant4(w, inv, ex != 255u), quant4(w + 4, inv, ex != 255u)};
+        if (c % kAct8Group == 0) a.e[g] = (uint8_t)ex;
+      }
+    }
+  }
+  if (!in_rows || n <= 0) return;
+  if constexpr (KIND == LinearKind::kForward) {
+    if (a.act != kActNone)
+      for (int j = 0; j < 8; ++j) v[j] = act(v[j], a.act);
+  } else if (a.act != kActNone) {
+    const lu2 u = *reinterpret_cast<const lu2*>(a.pq + g * kAct8Group + c % kAct8Group);
+    const float s = step_of(a.pe[g]);
+    for (int j = 0; j < 8; ++j) v[j] *= act_grad(dequant(u[j / 4], j % 4, s), a.act);
+  }
+  if (a.add) {
+    float w[8];
+    unpack(*reinterpret_cast<const lu4*>(static_cast<const T*>(a.add) + r * a.ldadd + c), w,
+           (const T*)nullptr);
+    for (int j = 0; j < 8; ++j) v[j] += w[j];
+  }
+  store8(static_cast<T*>(a.c) + r * a.ldc + c, n, v);
+}
+
+// The weight gradient's rows lie where their tensor lies in the flat gradient
+// row, at any alignment: vectors where that allows them.
+__device__ __forceinline__ bool grad_vec(const Linear& a) {
+  return ((uintptr_t)a.c & 15) == 0 && a.cols % 8 == 0 && a.ldg % 8 == 0;
+}
+
+__device__ __forceinline__ void store_grad(const Linear& a, bool vec, int32_t worker, int64_t r,
+                                           int32_t c, const float (&v)[8]) {
+  const int64_t at = (int64_t)worker * a.ldg + r * a.cols + c;
+  const int n = a.cols - c;
+  if (a.g_dtype == kGradF32) {
+    float* p = static_cast<float*>(a.c) + at;
+    if (vec) {
+      reinterpret_cast<lf4*>(p)[0] = lf4{v[0], v[1], v[2], v[3]};
+      reinterpret_cast<lf4*>(p)[1] = lf4{v[4], v[5], v[6], v[7]};
+    } else {
+      for (int j = 0; j < 8; ++j)
+        if (j < n) p[j] = v[j];
+    }
+  } else if (a.g_dtype == kGradF16) {
+    store8(static_cast<_Float16*>(a.c) + at, vec ? 8 : min(n, 7), v);
+    if (!vec && n >= 8) static_cast<_Float16*>(a.c)[at + 7] = (_Float16)v[7];
+  } else {
+    store8(static_cast<__bf16*>(a.c) + at, vec ? 8 : min(n, 7), v);
+    if (!vec && n >= 8) static_cast<__bf16*>(a.c)[at + 7] = (__bf16)v[7];
+  }
+}
+
+__device__ __forceinline__ void store_bias_grad(const Linear& a, int32_t worker, int64_t r,
+                                                float v) {
+  const int64_t at = (int64_t)worker * a.ldg + r;
+  if (a.g_dtype == kGradF32) static_cast<float*>(a.db)[at] = v;
+  else if (a.g_dtype == kGradF16) static_cast<_Float16*>(a.db)[at] = (_Float16)v;
+  else static_cast<__bf16*>(a.db)[at] = (__bf16)v;
+}
+
+// Partial sums of a split product: [split][worker][rows][cols8], then the
+// bias gradient's [split][worker][rows].
+__device__ __forceinline__ int64_t part_cols(const Linear& a) { return (a.cols + 7) / 8 * 8; }
+
+// ---- the product --------------------------------------------------------------------
+struct Tiles {
+  int32_t ta, tb;    // tiles along the result's columns and rows
+  int32_t splits;
+  int32_t ksteps;    // steps of kBK of one split
+};
+
+// Blocks are handed to the 8 XCDs in turn; this gives each XCD a range of
+// neighbouring tiles, so that its L2 sees an operand's rows once.
+__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
+  const int64_t q = total / 8, r = total % 8, x = id % 8, i = id / 8;
+  return x * q + min(x, r) + i;
+}
+
+template <typename T, LinearKind KIND, int BA, int BB, int WA, int WB>
+__global__ __launch_bounds__(WA* WB * 64, 2) void k_linear(Linear a, Tiles t) {
+  constexpr int NT = WA * WB * 64;
+  constexpr int ASRC = KIND == LinearKind::kForward ? kKRow
+                       : KIND == LinearKind::kInputGrad ? kKCol : kKept;
+  constexpr int BSRC = KIND == LinearKind::kWeightGrad ? kKCol : kKRow;
+  constexpr int TA = BA / WA / 16, TB = BB / WB / 16;
+  constexpr int kStageBytes = (BA + BB) * kBK * 2;
+  __shared__ __align__(1024) char lds[2 * kStageBytes];
+
+  const int64_t work = xcd_order(blockIdx.x, gridDim.x);
+  const int32_t tiles = t.ta * t.tb;
+  const int32_t tile = (int32_t)(work % tiles);
+  const int32_t rest = (int32_t)(work / tiles);
+  const int32_t split = rest % t.splits, worker = rest / t.splits;
+  // four rows of tiles together, along the columns: the tiles that run at one
+  // time share operands of both sides
+  const int32_t super = tile / (4 * t.ta), in = tile - super * 4 * t.ta;
+  const int32_t high = min(4, t.tb - super * 4);
+  const int32_t r0 = (super * 4 + in % high) * BB, c0 = in / high * BA;
+
+  const int64_t kbeg = (int64_t)split * t.ksteps * kBK;
+  const int64_t kend = min(a.k, kbeg + (int64_t)t.ksteps * kBK);
+  const uint32_t eld = (uint32_t)((a.cols + kAct8Group - 1) / kAct8Group);
+  const char* ap;
+  const uint8_t* ae = nullptr;
+  int64_t astep, bstep;  // bytes of one step along k
+  if constexpr (ASRC == kKRow) {
+    ap = static_cast<const char*>(a.a) + ((int64_t)c0 * a.lda + kbeg) * 2;
+    astep = kBK * 2;
+  } else {
+    constexpr int S = ASRC == kKept ? 1 : 2;
+    const int64_t k0 = (KIND == LinearKind::kWeightGrad ? worker * a.k : 0) + kbeg;
+    ap = static_cast<const char*>(a.a) + (k0 * a.lda + c0) * S;
+    astep = kBK * a.lda * S;
+    if constexpr (ASRC == kKept) ae = a.ae + k0 * eld + c0 / kAct8Group;
+  }
+  const char* bp;
+  if constexpr (BSRC == kKRow) {
+    bp = static_cast<const char*>(a.b) + ((int64_t)r0 * a.ldb + kbeg) * 2;
+    bstep = kBK * 2;
+  } else {
+    bp = static_cast<const char*>(a.b) + (((int64_t)worker * a.k + kbeg) * a.ldb + r0) * 2;
+    bstep = kBK * a.ldb * 2;
+  }
+
+  Stage<T, ASRC, BA, NT> sa;
+  Stage<T, BSRC, BB, NT> sb;
+  sa.init(c0, a.cols, (uint32_t)a.lda, eld);
+  sb.init(r0, (int32_t)min(a.rows, (int64_t)0x7FFFFFFF), (uint32_t)a.ldb, 0);
+
+  const int wave = threadIdx.x >> 6, wa = wave % WA, wb = wave / WA;
+  lf4 acc[TA][TB];
+#pragma unroll
+  for (int i = 0; i < TA; ++i)
+#pragma unroll
+    for (int j = 0; j < TB; ++j) acc[i][j] = lf4{0.0f, 0.0f, 0.0f, 0.0f};
+  // the bias gradient: the product with a row of ones, by the waves that hold
+  // the result's first columns
+  const bool ones = KIND == LinearKind::kWeightGrad && a.db && c0 == 0 && wa == 0;
+  lf4 accb[KIND == LinearKind::kWeightGrad ? TB : 1];
+  for (auto& v : accb) v = lf4{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint32_t one2 = pack2(1.0f, 1.0f, (const T*)nullptr);
+  const lu4 one8 = {one2, one2, one2, one2};
+
+  auto load = [&](int64_t k) {
+    const int64_t left = kend - k;
+    if (left >= kBK) {
+      sa.template load<false>(ap, ae, kBK, (uint32_t)a.lda, eld);
+      sb.template load<false>(bp, nullptr, kBK, (uint32_t)a.ldb, 0);
+    } else {
+      sa.template load<true>(ap, ae, (int32_t)left, (uint32_t)a.lda, eld);
+      sb.template load<true>(bp, nullptr, (int32_t)left, (uint32_t)a.ldb, 0);
+    }
+    ap += astep;
+    bp += bstep;
+    if constexpr (ASRC == kKept) ae += (int64_t)kBK * eld;
+  };
+
+  if (kbeg < kend) load(kbeg);
+  int buf = 0;
+  for (int64_t k = kbeg; k < kend; k += kBK) {
+    char* la = lds + buf * kStageBytes;
+    char* lb = la + BA * kBK * 2;
+    sa.store(la);
+    sb.store(lb);
+    // a barrier a step: the other half is written only after every wave has
+    // passed the next one, and so has read this half
+    __syncthreads();
+    if (k + kBK < kend) load(k + kBK);
+#pragma unroll
+    for (int ks = 0; ks < kBK / 32; ++ks) {
+      lu4 fa[TA], fb[TB];
+#pragma unroll
+      for (int i = 0; i < TA; ++i) fa[i] = fragment<ASRC, BA>(la, (wa * TA + i) * 16, ks);
+#pragma unroll
+      for (int j = 0; j < TB; ++j) fb[j] = fragment<BSRC, BB>(lb, (wb * TB + j) * 16, ks);
+#pragma unroll
+      for (int j = 0; j < TB; ++j)
+#pragma unroll
+        for (int i = 0; i < TA; ++i) acc[i][j] = mfma(fa[i], fb[j], acc[i][j], (const T*)nullptr);
+      if constexpr (KIND == LinearKind::kWeightGrad) {
+        if (ones) {
+#pragma unroll
+          for (int j = 0; j < TB; ++j) accb[j] = mfma(one8, fb[j], accb[j], (const T*)nullptr);
+        }
+      }
+    }
+    buf ^= 1;
+  }
+
+  // The results go through LDS, 16 rows of a wave at a time and within the
+  // wave alone: lane l holds row l % 16 and four columns of each tile, and
+  // takes back eight consecutive columns, so that a row's stores and operands
+  // are whole lines.
+  constexpr int kRow = TA * 16 + 4;  // floats of a row in LDS, off the bank period
+  constexpr int kLanes = TA * 2;     // lanes of a row
+  static_assert(WA * WB * 16 * kRow * 4 <= 2 * kStageBytes, "epilogue rows fit the stages");
+  const int l = threadIdx.x & 63;
+  float* rows = reinterpret_cast<float*>(lds) + wave * 16 * kRow;
+  const bool vec = KIND == LinearKind::kWeightGrad && grad_vec(a);
+  const int64_t pc = part_cols(a), wrow = ((int64_t)split * a.n + worker) * a.rows;
+  __syncthreads();  // every wave has read its last fragments
+#pragma unroll 1
+  for (int j = 0; j < TB; ++j) {
+    const int64_t rj = r0 + (wb * TB + j) * 16;
+#pragma unroll
+    for (int jj = 0; jj < TB; ++jj) {
+      if (jj != j) continue;  // a constant index into the accumulators
+#pragma unroll
+      for (int i = 0; i < TA; ++i)
+        *reinterpret_cast<lf4*>(rows + (l & 15) * kRow + i * 16 + (l >> 4) * 4) = acc[i][jj];
+      if constexpr (KIND == LinearKind::kWeightGrad) {
+        if (ones && l < 16 && rj + l < a.rows) {
+          if (t.splits > 1)
+            a.part[(int64_t)t.splits * a.n * a.rows * pc + wrow + rj + l] = accb[jj][0];
+          else
+            store_bias_grad(a, worker, rj + l, accb[jj][0]);
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll 1
+    for (int i = 0; i < 16 * kLanes; i += 64) {
+      const int rr = (i + l) / kLanes, cc = (i + l) % kLanes * 8;
+      const int64_t r = rj + rr;
+      const int32_t c = c0 + wa * TA * 16 + cc;
+      const bool in_rows = r < a.rows;
+      const lf4 x = *reinterpret_cast<const lf4*>(rows + rr * kRow + cc);
+      const lf4 y = *reinterpret_cast<const lf4*>(rows + rr * kRow + cc + 4);
+      float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      if (t.splits > 1) {
+        if (in_rows && c < a.cols) {
+          lf4* p = reinterpret_cast<lf4*>(a.part + (wrow + r) * pc + c);
+          p[0] = x;
+          p[1] = y;
+        }
+      } else if constexpr (KIND == LinearKind::kWeightGrad) {
+        if (in_rows && c < a.cols) store_grad(a, vec, worker, r, c, v);
+      } else {
+        finish<T, KIND>(a, in_rows, r, c, v);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+// ---- joining a split product ------------------------------------------------------
+// A thread adds eight columns' sums in split order and finishes them as above;
+// four lanes hold a group of 32 columns.
+template <typename T, LinearKind KIND>
+__global__ __launch_bounds__(256) void k_linear_join(Linear a, int32_t splits) {
+  const int32_t per_row = (a.cols + kAct8Group - 1) / kAct8Group * 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t wr = i / per_row;  // worker * rows + row
+  const int32_t c = (int32_t)(i - wr * per_row) * 8;
+  const int64_t pc = part_cols(a), all = a.n * a.rows;
+  if (wr >= all) return;  // whole groups of lanes
+  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < a.cols) {
+    for (int32_t s = 0; s < splits; ++s) {
+      const lf4* p = reinterpret_cast<const lf4*>(a.part + ((int64_t)s * all + wr) * pc + c);
+      const lf4 x = p[0], y = p[1];
+      for (int j = 0; j < 4; ++j) {
+        v[j] += x[j];
+        v[4 + j] += y[j];
+      }
+    }
+  }
+  if constexpr (KIND == LinearKind::kWeightGrad) {
+    const int32_t worker = (int32_t)(wr / a.rows);
+    const int64_t r = wr - worker * a.rows;
+    if (c < a.cols) store_grad(a, grad_vec(a), worker, r, c, v);
+    if (c == 0 && a.db) {
+      float s = 0.0f;
+      for (int32_t p = 0; p < splits; ++p)
+        s += a.part[(int64_t)splits * all * pc + (int64_t)p * all + wr];
+      store_bias_grad(a, worker, r, s);
+    }
+  } else {
+    finish<T, KIND>(a, true, wr, c, v);
+  }
+}
+
+// ---- host side ----------------------------------------------------------------------
+constexpr int kCUs = 256;
+
+struct Choice {
+  bool big;
+  Tiles t;
+};
+
+int64_t tiles_of(int64_t rows, int64_t cols, int tile) {
+  return ((rows + tile - 1) / tile) * ((cols + tile - 1) / tile);
+}
+
+Choice choose(int32_t n, int64_t rows, int32_t cols, int64_t k) {
+  Choice c;
+  c.big = tiles_of(rows, cols, 256) * n >= kCUs * 3 / 4;
+  const int tile = c.big ? 256 : 128;
+  c.t.ta = (int32_t)((cols + tile - 1) / tile);
+  c.t.tb = (int32_t)((rows + tile - 1) / tile);
+  const int64_t all = tiles_of(rows, cols, tile) * n, steps = (k + kBK - 1) / kBK;
+  int64_t splits = 1;
+  // a product of few tiles: up to two blocks to a CU, at least four steps each
+  if (!c.big && all <= kCUs)
+    splits = std::max<int64_t>(1, std::min<int64_t>(2 * kCUs / all, steps / 4));
+  c.t.ksteps = (int32_t)std::max<int64_t>(1, (steps + splits - 1) / splits);
+  c.t.splits = (int32_t)std::max<int64_t>(1, (steps + c.t.ksteps - 1) / c.t.ksteps);
+  return c;
+}
+
+template <typename T, LinearKind KIND>
+void product(const Linear& a, hipStream_t st) {
+  const Choice c = choose(a.n, a.rows, a.cols, a.k);
+  const uint32_t grid = (uint32_t)((int64_t)c.t.ta * c.t.tb * c.t.splits * a.n);
+  if (c.big)
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear<T, KIND, 256, 256, 2, 4>), dim3(grid), dim3(512),
+                       0, st, a, c.t);
+  else
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear<T, KIND, 128, 128, 2, 2>), dim3(grid), dim3(256),
+                       0, st, a, c.t);
+}
+
+template <typename T, LinearKind KIND>
+void join(const Linear& a, hipStream_t st) {
+  const Choice c = choose(a.n, a.rows, a.cols, a.k);
+  const int64_t lanes = (int64_t)a.n * a.rows * ((a.cols + kAct8Group - 1) / kAct8Group) * 4;
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_join<T, KIND>), dim3((uint32_t)((lanes + 255) / 256)),
+                     dim3(256), 0, st, a, c.t.splits);
+}
+
+template <typename T>
+void product(LinearKind kind, const Linear& a, hipStream_t st) {
+  if (kind == LinearKind::kForward) product<T, LinearKind::kForward>(a, st);
+  else if (kind == LinearKind::kInputGrad) product<T, LinearKind::kInputGrad>(a, st);
+  else product<T, LinearKind::kWeightGrad>(a, st);
+}
+
+template <typename T>
+void join(LinearKind kind, const Linear& a, hipStream_t st) {
+  if (kind == LinearKind::kForward) join<T, LinearKind::kForward>(a, st);
+  else if (kind == LinearKind::kInputGrad) join<T, LinearKind::kInputGrad>(a, st);
+  else join<T, LinearKind::kWeightGrad>(a, st);
+}
+
+}  // namespace
+
+int32_t linear_splits(LinearKind, int32_t n, int64_t rows, int32_t cols, int64_t k) {
+  return choose(n, rows, cols, k).t.splits;
+}
+
+size_t linear_workspace(LinearKind kind, int32_t n, int64_t rows, int32_t cols, int64_t k) {
+  const int32_t s = linear_splits(kind, n, rows, cols, k);
+  if (s <= 1) return 0;
+  const size_t pc = (size_t)(cols + 7) / 8 * 8;
+  return (size_t)s * n * rows * (pc + (kind == LinearKind::kWeightGrad ? 1 : 0)) * 4;
+}
+
+void launch_linear(LinearKind kind, const Linear& a, hipStream_t st) {
+  if (a.dtype == kGradF16) product<_Float16>(kind, a, st);
+  else product<__bf16>(kind, a, st);
+}
+
+void launch_linear_join(LinearKind kind, const Linear& a, hipStream_t st) {
+  if (a.dtype == kGradF16) join<_Float16>(kind, a, st);
+  else join<__bf16>(kind, a, st);
+}
+
+}  // namespace oba

@@ -391,6 +391,104 @@ int oba_step_small(oba_layout layout, const void* g, int g_dtype, const float* m
                    const float* denom, float* m_out, float* x, double beta1, double lr,
                    hipStream_t stream);
 
+/* ---- layers: norm, linear, activations kept in 8 bits ----------------------
+ * What a training pass computes between the parameters x and the gradient
+ * rows g: the forward and backward passes of a layer norm and of a linear
+ * layer, with the activations that the backward pass needs kept in 8 bits.
+ * ([AIMech] definition: x_t and the workers' stochastic gradients g_t of the
+ * model; limitations: memory is what the method's users run out of.)  These
+ * calls take no layout handle.
+ *
+ * Matrices are rows of ld elements, row-major: 16-byte aligned, ld a multiple
+ * of 8 and at least the columns, at most 2^22.  A row may be read up to its
+ * columns rounded up to 8 (also the last row); what lies there does not
+ * change results, and only the named columns are written.  At most 2^30 rows
+ * and 2^20 columns (2^14 for a layer norm).  gamma, beta and bias are
+ * binary32 vectors at any multiple of 4 bytes, so slices of the flat x serve.
+ * With n workers, worker i's rows are [i*rows, (i+1)*rows), and its gradient
+ * of a parameter tensor goes to where the tensor lies in its row of g:
+ * pointers to the tensor's place in row 0, ldg elements from worker to
+ * worker, any alignment of the element.  Gradients are written, not added to;
+ * those of no rows are 0.
+ *
+ * Arithmetic is binary32 (products of 16-bit operands exact, sums binary32 in
+ * a fixed order), rounded once to each output: results are reproducible.  No
+ * call allocates, and one workspace serves one call at a time.  rows = 0 is
+ * allowed.
+ *
+ * 8-bit form of a [rows][cols] matrix: G = ceil(cols / 32) groups of 32
+ * columns; q: [rows][32*G] integers (16-byte aligned, those past cols 0), e:
+ * [rows][G] exponent bytes.  For a group of largest magnitude f * 2^k
+ * (1 <= f < 2) the step is 2^j, j = max(k - 6, -126), the byte j + 127 and an
+ * element x the integer x / 2^j, rounded to nearest (ties to even) and held to
+ * +-127: within half a step of x, or one step above 127.5 steps.  A group
+ * holding an infinity or a NaN has the byte 255 and stands for 32 NaN. */
+#define OBA_ACT8_GROUP 32
+int oba_act8_encode(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dtype, int8_t* q,
+                    uint8_t* e, hipStream_t stream);
+/* The values, rounded to dtype (exact in binary32 and bfloat16, and in
+ * binary16 for what was encoded from it). */
+int oba_act8_decode(int64_t rows, int64_t cols, const int8_t* q, const uint8_t* e, void* x,
+                    int64_t ldx, int dtype, hipStream_t stream);
+
+/* y = xhat * gamma + beta, xhat = (x - mean) * rstd, rstd = 1 / sqrt(var + eta)
+ * per row, var the mean square of x - mean.  mean, rstd: [rows] binary32 out.
+ * q, e: NULL, or xhat kept in 8 bits for the backward pass.  eta >= 0. */
+int oba_layer_norm(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dtype,
+                   const float* gamma, const float* beta, double eta, void* y, int64_t ldy,
+                   float* mean, float* rstd, int8_t* q, uint8_t* e, hipStream_t stream);
+
+/* With a = dy * gamma:  dx = rstd * (a - mean(a) - xhat * mean(a * xhat)) + add,
+ * and for each of n workers dgamma = sum dy * xhat, dbeta = sum dy over its
+ * rows.  xhat comes from x and mean (q = e = NULL), or from q, e (x = mean =
+ * NULL).  add: [n*rows] rows (the gradient that goes round the layer) or NULL.
+ * ws: at least oba_layer_norm_backward_workspace_bytes(), 16-byte aligned. */
+size_t oba_layer_norm_backward_workspace_bytes(int32_t n, int64_t rows, int64_t cols);
+int oba_layer_norm_backward(int32_t n, int64_t rows, int64_t cols, const void* dy, int64_t lddy,
+                            int dtype, const void* x, int64_t ldx, const float* mean,
+                            const int8_t* q, const uint8_t* e, const float* rstd,
+                            const float* gamma, const void* add, int64_t ldadd, void* dx,
+                            int64_t lddx, void* dgamma, void* dbeta, int g_dtype, int64_t ldg,
+                            void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Activation functions: the identity; max(p, 0), its derivative 0 at 0; p *
+ * Phi(p) with the normal distribution function; and that with (1 +
+ * tanh(sqrt(2/pi) * (p + 0.044715 p^3))) / 2 in Phi's place. */
+enum { OBA_ACT_NONE = 0, OBA_ACT_RELU = 1, OBA_ACT_GELU = 2, OBA_ACT_GELU_TANH = 3 };
+
+/* p = x w^T + bias;  y = act(p) + residual.  x: [rows][in], w: [out][in], y and
+ * residual: [rows][out], all of dtype OBA_F16 or OBA_BF16 (others are
+ * OBA_EINVAL); bias, residual: or NULL.  q, e: NULL, or p kept in 8 bits for
+ * the backward pass (from its binary32 value).  ws: at least
+ * oba_linear_workspace_bytes() (which serves oba_linear_input_grad of the same
+ * sizes too; it may be 0, and ws then NULL), 16-byte aligned. */
+size_t oba_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out);
+int oba_linear(int64_t rows, int64_t in, int64_t out, const void* x, int64_t ldx, const void* w,
+               int64_t ldw, int dtype, const float* bias, int act, const void* residual,
+               int64_t ldr, void* y, int64_t ldy, int8_t* q, uint8_t* e, void* ws,
+               size_t ws_bytes, hipStream_t stream);
+
+/* dx = (dy w) * act'(p) + add.  dy: [rows][out], w: [out][in], dx and add:
+ * [rows][in].  p is the kept pre-activation that the layer's input x = act(p)
+ * came from (q, e: [rows][in] in 8 bits; NULL for OBA_ACT_NONE and only then).
+ * add: or NULL.  ws as for oba_linear. */
+int oba_linear_input_grad(int64_t rows, int64_t in, int64_t out, const void* dy, int64_t lddy,
+                          const void* w, int64_t ldw, int dtype, int act, const int8_t* q,
+                          const uint8_t* e, const void* add, int64_t ldadd, void* dx,
+                          int64_t lddx, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* For each of n workers dw = dy^T x and db = column sums of dy over its rows.
+ * dy: [n*rows][out] of dtype OBA_F16 or OBA_BF16; x: [n*rows][in] kept in 8
+ * bits (q, e), its values taken in dtype (for OBA_F16 rounded to it, which
+ * changes only what was not encoded from binary16).  dw: [out][in], db: [out]
+ * or NULL, in g_dtype.  ws: at least oba_linear_weight_grad_workspace_bytes(),
+ * 16-byte aligned (NULL if that is 0). */
+size_t oba_linear_weight_grad_workspace_bytes(int32_t n, int64_t rows, int64_t in, int64_t out);
+int oba_linear_weight_grad(int32_t n, int64_t rows, int64_t in, int64_t out, const void* dy,
+                           int64_t lddy, int dtype, const int8_t* q, const uint8_t* e, void* dw,
+                           void* db, int g_dtype, int64_t ldg, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
+
 /* ---- kernel timing (measurement aid) ---------------------------------------
  * While enabled, every kernel the library launches is bracketed by two HIP
  * events on the launch stream (up to `capacity` launches are kept).
@@ -400,7 +498,9 @@ int oba_step_small(oba_layout layout, const void* g, int g_dtype, const float* m
  * "server_p1", "server_p2", "decompress_update", "adam_warmup",
  * "freeze_variance", "compress_deferred", "server_deferred",
  * "deferred_errors", "server_momentum", "compress_deferred_local",
- * "step_small"; the listed entry points record under the names of their flat
+ * "step_small", "act8_encode", "act8_decode", "layer_norm",
+ * "layer_norm_backward", "linear", "linear_input_grad", "linear_weight_grad"
+ * (each of these one record per call, all of its kernels in it); the listed entry points record under the names of their flat
  * forms; "adam_warmup" includes the norm kernel of
  * oba_adam_warmup_step_vnorm).  oba_timing_reset drops all records. */
 int oba_timing_enable(int on, int32_t capacity);

@@ -1,0 +1,142 @@
+"""Refusals of the layer operators: argument errors are found on the host,
+before any HIP call, so made-up addresses serve and nothing is launched."""
+import ctypes
+
+import pytest
+
+from communication_compressed_optimizer_02_amd import binding as oba
+
+EINVAL, EALIGN, EWORKSPACE = -1, -2, -4
+F32, F16, BF16 = 0, 1, 2
+A = 0x1000  # an aligned address that no call may touch
+
+
+def call(name, base, **change):
+    """The entry point with base's arguments (in order), some changed."""
+    args = dict(base)
+    assert set(change) <= set(args), set(change) - set(args)
+    args.update(change)
+    fn = getattr(oba.lib(), name)
+    return fn(*[ctypes.c_void_p(v) if t is ctypes.c_void_p else v
+                for v, t in zip(args.values(), fn.argtypes)])
+
+
+ENCODE = dict(rows=4, cols=40, x=A, ldx=40, dtype=BF16, q=A, e=A, stream=None)
+DECODE = dict(rows=4, cols=40, q=A, e=A, x=A, ldx=40, dtype=BF16, stream=None)
+NORM = dict(rows=4, cols=40, x=A, ldx=40, dtype=BF16, gamma=A, beta=A, eta=1e-5, y=A, ldy=40,
+            mean=A, rstd=A, q=None, e=None, stream=None)
+NORM_B = dict(n=2, rows=4, cols=40, dy=A, lddy=40, dtype=BF16, x=A, ldx=40, mean=A, q=None,
+              e=None, rstd=A, gamma=A, add=None, ldadd=0, dx=A, lddx=40, dgamma=A, dbeta=A,
+              g_dtype=F16, ldg=80, ws=A, ws_bytes=1 << 20, stream=None)
+LINEAR = dict(rows=4, n_in=2048, n_out=64, x=A, ldx=2048, w=A, ldw=2048, dtype=BF16, bias=A, act=2,
+              residual=A, ldr=64, y=A, ldy=64, q=A, e=A, ws=A, ws_bytes=1 << 24, stream=None)
+INPUT = dict(rows=4, n_in=64, n_out=2048, dy=A, lddy=2048, w=A, ldw=64, dtype=F16, act=2, q=A,
+             e=A, add=A, ldadd=64, dx=A, lddx=64, ws=A, ws_bytes=1 << 24, stream=None)
+WEIGHT = dict(n=2, rows=2048, n_in=64, n_out=64, dy=A, lddy=64, dtype=F16, q=A, e=A, dw=A, db=A,
+              g_dtype=F32, ldg=64 * 65, ws=A, ws_bytes=1 << 24, stream=None)
+
+CASES = [
+    ("oba_act8_encode", ENCODE, [
+        (dict(rows=-1), EINVAL), (dict(rows=(1 << 30) + 1), EINVAL), (dict(cols=0), EINVAL),
+        (dict(cols=(1 << 20) + 1, ldx=1 << 21), EINVAL), (dict(ldx=36), EINVAL),
+        (dict(ldx=44), EINVAL), (dict(ldx=(1 << 22) + 8), EINVAL), (dict(dtype=3), EINVAL),
+        (dict(dtype=-1), EINVAL), (dict(x=None), EINVAL), (dict(x=A + 8), EALIGN),
+        (dict(q=None), EINVAL), (dict(e=None), EINVAL), (dict(q=A + 4), EALIGN),
+        (dict(rows=1 << 30, cols=1 << 13, ldx=1 << 13), EINVAL)]),
+    ("oba_act8_decode", DECODE, [
+        (dict(rows=-1), EINVAL), (dict(cols=0), EINVAL), (dict(ldx=32), EINVAL),
+        (dict(dtype=9), EINVAL), (dict(x=None), EINVAL), (dict(x=A + 2), EALIGN),
+        (dict(q=None), EINVAL), (dict(e=None), EINVAL), (dict(q=A + 8), EALIGN)]),
+    ("oba_layer_norm", NORM, [
+        (dict(rows=-1), EINVAL), (dict(cols=0), EINVAL),
+        (dict(cols=16385, ldx=16392, ldy=16392), EINVAL), (dict(ldx=32), EINVAL),
+        (dict(ldy=41), EINVAL), (dict(dtype=3), EINVAL), (dict(eta=-1.0), EINVAL),
+        (dict(eta=float("nan")), EINVAL), (dict(eta=float("inf")), EINVAL),
+        (dict(x=None), EINVAL), (dict(gamma=None), EINVAL), (dict(beta=None), EINVAL),
+        (dict(mean=None), EINVAL), (dict(rstd=None), EINVAL), (dict(y=None), EINVAL),
+        (dict(gamma=A + 2), EALIGN), (dict(y=A + 8), EALIGN), (dict(q=A), EINVAL),
+        (dict(e=A), EINVAL), (dict(q=A + 8, e=A), EALIGN)]),
+    ("oba_layer_norm_backward", NORM_B, [
+        (dict(n=0), EINVAL), (dict(n=4097), EINVAL), (dict(rows=-1), EINVAL),
+        (dict(rows=1 << 30), EINVAL), (dict(cols=0), EINVAL), (dict(dtype=3), EINVAL),
+        (dict(g_dtype=3), EINVAL), (dict(lddy=39), EINVAL), (dict(lddx=8), EINVAL),
+        (dict(ldx=8), EINVAL), (dict(add=A, ldadd=8), EINVAL), (dict(ldg=39), EINVAL),
+        (dict(x=None), EINVAL), (dict(mean=None), EINVAL), (dict(q=A, e=A), EINVAL),
+        (dict(x=None, mean=None, q=A), EINVAL), (dict(x=None, mean=None, e=A), EINVAL),
+        (dict(x=None, mean=None, q=A + 8, e=A), EALIGN), (dict(dgamma=None), EINVAL),
+        (dict(dbeta=None), EINVAL), (dict(dgamma=A + 1), EALIGN), (dict(dy=None), EINVAL),
+        (dict(dy=A + 8), EALIGN), (dict(rstd=None), EINVAL), (dict(gamma=None), EINVAL),
+        (dict(dx=None), EINVAL), (dict(ws=None), EINVAL), (dict(ws=A + 8), EALIGN),
+        (dict(ws_bytes=8), EWORKSPACE)]),
+    ("oba_linear", LINEAR, [
+        (dict(rows=-1), EINVAL), (dict(n_in=0), EINVAL), (dict(n_out=0), EINVAL),
+        (dict(n_out=(1 << 20) + 8, ldy=1 << 21, ldr=1 << 21), EINVAL), (dict(dtype=F32), EINVAL),
+        (dict(act=4), EINVAL), (dict(act=-1), EINVAL), (dict(ldx=2040), EINVAL),
+        (dict(ldw=2049), EINVAL), (dict(ldy=56), EINVAL), (dict(ldr=60), EINVAL),
+        (dict(x=None), EINVAL), (dict(w=None), EINVAL), (dict(y=None), EINVAL),
+        (dict(x=A + 2), EALIGN), (dict(w=A + 4), EALIGN), (dict(residual=A + 8), EALIGN),
+        (dict(bias=A + 1), EALIGN), (dict(q=None), EINVAL), (dict(e=None), EINVAL),
+        (dict(ws=None), EINVAL), (dict(ws=A + 4), EALIGN), (dict(ws_bytes=0), EWORKSPACE)]),
+    ("oba_linear_input_grad", INPUT, [
+        (dict(rows=-1), EINVAL), (dict(n_in=0), EINVAL), (dict(n_out=0), EINVAL),
+        (dict(dtype=F32), EINVAL), (dict(act=7), EINVAL), (dict(act=0), EINVAL),
+        (dict(q=None, e=None), EINVAL), (dict(q=None), EINVAL), (dict(e=None), EINVAL),
+        (dict(q=A + 8), EALIGN), (dict(lddy=2040), EINVAL), (dict(ldw=60), EINVAL),
+        (dict(lddx=60), EINVAL), (dict(ldadd=60), EINVAL), (dict(dy=None), EINVAL),
+        (dict(w=None), EINVAL), (dict(dx=None), EINVAL), (dict(dx=A + 8), EALIGN),
+        (dict(ws=None), EINVAL), (dict(ws_bytes=64), EWORKSPACE)]),
+    ("oba_linear_weight_grad", WEIGHT, [
+        (dict(n=0), EINVAL), (dict(n=4097), EINVAL), (dict(rows=-1), EINVAL),
+        (dict(n_in=0), EINVAL), (dict(n_out=0), EINVAL), (dict(dtype=F32), EINVAL),
+        (dict(g_dtype=5), EINVAL), (dict(lddy=60), EINVAL), (dict(ldg=64 * 64 - 1), EINVAL),
+        (dict(dw=None), EINVAL), (dict(dw=A + 2), EALIGN), (dict(db=A + 1), EALIGN),
+        (dict(dy=None), EINVAL), (dict(dy=A + 8), EALIGN), (dict(q=None), EINVAL),
+        (dict(e=None), EINVAL), (dict(q=A + 1), EALIGN), (dict(ws=None), EINVAL),
+        (dict(ws_bytes=0), EWORKSPACE)]),
+]
+
+
+@pytest.mark.parametrize("name,base,change,expect",
+                         [(n, b, c, x) for n, b, cs in CASES for c, x in cs])
+def test_refused(name, base, change, expect):
+    assert call(name, base, **change) == expect, change
+
+
+@pytest.mark.parametrize("name,base", [
+    ("oba_act8_encode", ENCODE), ("oba_act8_decode", DECODE), ("oba_layer_norm", NORM),
+    ("oba_linear", LINEAR), ("oba_linear_input_grad", INPUT)])
+def test_no_rows_need_no_memory(name, base):
+    """rows = 0 returns before a pointer is looked at (no launch, no device)."""
+    none = {k: None for k, v in base.items() if v == A and k != "stream"}
+    assert call(name, base, rows=0, **none) == 0
+
+
+def test_workspace_sizes():
+    """The workspace holds what a call needs: one product of few tiles is
+    split, a large one is not, and sizes that are refused need none."""
+    L = oba.lib()
+    assert L.oba_linear_workspace_bytes(1, 2048, 64) > 0
+    assert L.oba_linear_workspace_bytes(16384, 1024, 4096) == 0
+    assert L.oba_linear_workspace_bytes(0, 64, 64) == 0
+    assert L.oba_linear_workspace_bytes(-1, 64, 64) == 0
+    assert L.oba_linear_weight_grad_workspace_bytes(2, 2048, 64, 64) > 0
+    assert L.oba_linear_weight_grad_workspace_bytes(8, 2048, 1024, 4096) == 0
+    assert L.oba_linear_weight_grad_workspace_bytes(0, 2048, 64, 64) == 0
+    b = L.oba_layer_norm_backward_workspace_bytes(2, 4, 40)
+    assert b >= 2 * 2 * 40 * 4
+    assert L.oba_layer_norm_backward_workspace_bytes(2, 4, 1 << 20) == 0
+
+
+
+
+def test_binding_refuses_host_tensors_and_unknown_activations(monkeypatch):
+    import torch
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x = torch.zeros(4, 40)
+    q, e = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 2, dtype=torch.uint8)
+    with pytest.raises(TypeError):
+        oba.act8_encode(x, q, e)
+    with pytest.raises(TypeError):
+        oba.act8_decode(q, e, [1.0])
+    assert set(oba.ACTS) == {"none", "relu", "gelu", "gelu_tanh"}
