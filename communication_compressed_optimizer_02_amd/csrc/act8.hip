@@ -75,16 +75,16 @@ __global__ __launch_bounds__(kA8Block) void k_act8_encode(int64_t pieces, int32_
   for (int u = 0; u < kA8Unroll; ++u) {
     uint32_t top = 0;
     for (int j = 0; j < V; ++j) top = max(top, magnitude(v[u][j]));
-    for (int m = 1; m < L; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+    top = max_lanes<L>(top);
     const uint32_t ex = group_exp(top);
-    const float inv = inv_step_of(ex);
+    const float inv = inv_step_of(ex), step = step_of(ex);
     if (row[u] < 0) continue;
     const int64_t at = (row[u] * per_row + piece[u]) * V;
     if constexpr (V == 8) {
-      const lu2 o = {quant4(v[u], inv, ex != 255u), quant4(v[u] + 4, inv, ex != 255u)};
+      const lu2 o = {quant4(v[u], inv, step, ex != 255u), quant4(v[u] + 4, inv, step, ex != 255u)};
       *reinterpret_cast<lu2*>(q + at) = o;
     } else {
-      *reinterpret_cast<uint32_t*>(q + at) = quant4(v[u], inv, ex != 255u);
+      *reinterpret_cast<uint32_t*>(q + at) = quant4(v[u], inv, step, ex != 255u);
     }
     if ((threadIdx.x & (L - 1)) == 0) e[at / kAct8Group] = (uint8_t)ex;
   }

@@ -176,49 +176,76 @@ __device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
   }
 }
 
+// What the epilogue reads for eight results, loaded ahead of their use (a
+// load behind each use left the epilogue waiting: 107 of 255 us at 16384 x
+// 1024 -> 4096 for the bias alone).
+struct Extra {
+  lu2 u;        // kept pre-activation of the derivative
+  uint32_t e;
+  lu4 add;      // residual
+};
+
+template <LinearKind KIND>
+__device__ __forceinline__ void load_extra(const Linear& a, int64_t r, int32_t c, Extra& x) {
+  if (r >= a.rows || c >= a.cols) return;
+  if constexpr (KIND == LinearKind::kInputGrad) {
+    if (a.act != kActNone) {
+      const int64_t g = r * ((a.cols + kAct8Group - 1) / kAct8Group) + c / kAct8Group;
+      x.u = *reinterpret_cast<const lu2*>(a.pq + g * kAct8Group + c % kAct8Group);
+      x.e = a.pe[g];
+    }
+  }
+  if (a.add)
+    x.add = *reinterpret_cast<const lu4*>(static_cast<const uint16_t*>(a.add) + r * a.ldadd + c);
+}
+
+__device__ __forceinline__ void load_bias(const Linear& a, int32_t c, float (&b)[8]) {
+  for (int j = 0; j < 8; ++j) b[j] = a.bias && c + j < a.cols ? a.bias[c + j] : 0.0f;
+}
+
 // The forward result from the product, the input gradient from the product:
 // bias, 8-bit pre-activation kept or used, activation or its derivative,
 // residual, one rounding.  Four neighbouring lanes hold a group of 32 columns.
 template <typename T, LinearKind KIND>
-__device__ __forceinline__ void finish(const Linear& a, bool in_rows, int64_t r, int32_t c,
-                                       float (&v)[8]) {
+__device__ __forceinline__ void finish(const Linear& a, int64_t r, int32_t c, const float (&b)[8],
+                                       const Extra& x, float (&v)[8]) {
   const int n = a.cols - c;
-  const int32_t groups = (a.cols + kAct8Group - 1) / kAct8Group;
-  const int64_t g = r * groups + c / kAct8Group;
+  const bool in_rows = r < a.rows;
   if constexpr (KIND == LinearKind::kForward) {
     if (a.bias)
-      for (int j = 0; j < 8; ++j) v[j] += j < n ? a.bias[c + j] : 0.0f;
+      for (int j = 0; j < 8; ++j) v[j] += b[j];
     if (a.q) {  // columns past the last are kept as 0
+      const int32_t groups = (a.cols + kAct8Group - 1) / kAct8Group;
       uint32_t top = 0;
       float w[8];
       for (int j = 0; j < 8; ++j) {
         w[j] = j < n ? v[j] : 0.0f;
         top = max(top, magnitude(w[j]));
       }
-      top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+      top = max_lanes<4>(top);
       const uint32_t ex = group_exp(top);
-      const float inv = inv_step_of(ex);
+      const float inv = inv_step_of(ex), step = step_of(ex);
       if (in_rows && c / kAct8Group < groups) {
+        const int64_t g = r * groups + c / kAct8Group;
         *reinterpret_cast<lu2*>(a.q + g * kAct8Group + c % kAct8Group) =
-            lu2{quant4(w, inv, ex != 255u), quant4(w + 4, inv, ex != 255u)};
+            lu2{quant4(w, inv, step, ex != 255u), quant4(w + 4, inv, step, ex != 255u)};
         if (c % kAct8Group == 0) a.e[g] = (uint8_t)ex;
       }
     }
   }
   if (!in_rows || n <= 0) return;
   if constexpr (KIND == LinearKind::kForward) {
-    if (a.act != kActNone)
-      for (int j = 0; j < 8; ++j) v[j] = act(v[j], a.act);
+    activate(v, a.act);
   } else if (a.act != kActNone) {
-    const lu2 u = *reinterpret_cast<const lu2*>(a.pq + g * kAct8Group + c % kAct8Group);
-    const float s = step_of(a.pe[g]);
-    for (int j = 0; j < 8; ++j) v[j] *= act_grad(dequant(u[j / 4], j % 4, s), a.act);
+    const float s = step_of(x.e);
+    float d[8];
+    for (int j = 0; j < 8; ++j) d[j] = dequant(x.u[j / 4], j % 4, s);
+    activate_grad(d, a.act);
+    for (int j = 0; j < 8; ++j) v[j] *= d[j];
   }
   if (a.add) {
     float w[8];
-    unpack(*reinterpret_cast<const lu4*>(static_cast<const T*>(a.add) + r * a.ldadd + c), w,
-           (const T*)nullptr);
+    unpack(x.add, w, (const T*)nullptr);
     for (int j = 0; j < 8; ++j) v[j] += w[j];
   }
   store8(static_cast<T*>(a.c) + r * a.ldc + c, n, v);
@@ -278,7 +305,7 @@ __device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
   return x * q + min(x, r) + i;
 }
 
-template <typename T, LinearKind KIND, int BA, int BB, int WA, int WB>
+template <typename T, LinearKind KIND, int BA, int BB, int WA, int WB, int BUFS>
 __global__ __launch_bounds__(WA* WB * 64, 2) void k_linear(Linear a, Tiles t) {
   constexpr int NT = WA * WB * 64;
   constexpr int ASRC = KIND == LinearKind::kForward ? kKRow
@@ -286,7 +313,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void k_linear(Linear a, Tiles t) {
   constexpr int BSRC = KIND == LinearKind::kWeightGrad ? kKCol : kKRow;
   constexpr int TA = BA / WA / 16, TB = BB / WB / 16;
   constexpr int kStageBytes = (BA + BB) * kBK * 2;
-  __shared__ __align__(1024) char lds[2 * kStageBytes];
+  __shared__ __align__(1024) char lds[BUFS * kStageBytes];
 
   const int64_t work = xcd_order(blockIdx.x, gridDim.x);
   const int32_t tiles = t.ta * t.tb;
@@ -386,7 +413,8 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void k_linear(Linear a, Tiles t) {
         }
       }
     }
-    buf ^= 1;
+    if constexpr (BUFS == 1) __syncthreads();  // all have read before the next is written
+    else buf ^= 1;
   }
 
   // The results go through LDS, 16 rows of a wave at a time and within the
@@ -395,15 +423,28 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void k_linear(Linear a, Tiles t) {
   // are whole lines.
   constexpr int kRow = TA * 16 + 4;  // floats of a row in LDS, off the bank period
   constexpr int kLanes = TA * 2;     // lanes of a row
-  static_assert(WA * WB * 16 * kRow * 4 <= 2 * kStageBytes, "epilogue rows fit the stages");
+  static_assert(WA * WB * 16 * kRow * 4 <= BUFS * kStageBytes, "epilogue rows fit the stages");
   const int l = threadIdx.x & 63;
   float* rows = reinterpret_cast<float*>(lds) + wave * 16 * kRow;
   const bool vec = KIND == LinearKind::kWeightGrad && grad_vec(a);
   const int64_t pc = part_cols(a), wrow = ((int64_t)split * a.n + worker) * a.rows;
   __syncthreads();  // every wave has read its last fragments
+  constexpr int kIter = 16 * kLanes / 64;
+  const int rr = l / kLanes, cc = l % kLanes * 8;  // the lane's first row, and its columns
+  const int32_t c = c0 + wa * TA * 16 + cc;
+  float bias[8];
+  if constexpr (KIND == LinearKind::kForward) load_bias(a, c, bias);
 #pragma unroll 1
   for (int j = 0; j < TB; ++j) {
     const int64_t rj = r0 + (wb * TB + j) * 16;
+    Extra extra[kIter];
+    if constexpr (KIND != LinearKind::kWeightGrad) {
+      if (t.splits == 1) {
+#pragma unroll
+        for (int i = 0; i < kIter; ++i)
+          load_extra<KIND>(a, rj + rr + i * (64 / kLanes), c, extra[i]);
+      }
+    }
 #pragma unroll
     for (int jj = 0; jj < TB; ++jj) {
       if (jj != j) continue;  // a constant index into the accumulators
@@ -422,31 +463,107 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void k_linear(Linear a, Tiles t) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll 1
-    for (int i = 0; i < 16 * kLanes; i += 64) {
-      const int rr = (i + l) / kLanes, cc = (i + l) % kLanes * 8;
-      const int64_t r = rj + rr;
-      const int32_t c = c0 + wa * TA * 16 + cc;
-      const bool in_rows = r < a.rows;
-      const lf4 x = *reinterpret_cast<const lf4*>(rows + rr * kRow + cc);
-      const lf4 y = *reinterpret_cast<const lf4*>(rows + rr * kRow + cc + 4);
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int ri = rr + i * (64 / kLanes);
+      const int64_t r = rj + ri;
+      const lf4 x = *reinterpret_cast<const lf4*>(rows + ri * kRow + cc);
+      const lf4 y = *reinterpret_cast<const lf4*>(rows + ri * kRow + cc + 4);
       float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
       if (t.splits > 1) {
-        if (in_rows && c < a.cols) {
+        if (r < a.rows && c < a.cols) {
           lf4* p = reinterpret_cast<lf4*>(a.part + (wrow + r) * pc + c);
           p[0] = x;
           p[1] = y;
         }
       } else if constexpr (KIND == LinearKind::kWeightGrad) {
-        if (in_rows && c < a.cols) store_grad(a, vec, worker, r, c, v);
+        if (r < a.rows && c < a.cols) store_grad(a, vec, worker, r, c, v);
       } else {
-        finish<T, KIND>(a, in_rows, r, c, v);
+        finish<T, KIND>(a, r, c, bias, extra[i], v);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
+}
+
+// ---- the forward product of few rows ----------------------------------------------
+// Up to 64 rows cost what reading w costs.  A block owns 32 columns (a group
+// of the 8-bit form); its 8 waves share k in lines of 64, each wave's
+// fragments straight from memory (a line of w is used by one wave, once), all
+// of a batch's loads before its products.  The waves' sums meet in LDS, added
+// in wave order.
+constexpr int kFewWaves = 8, kFewCols = 32;
+
+// The 8 elements of a row from k; those at or past K are 0.
+__device__ __forceinline__ lu4 load_k(const uint16_t* row, int64_t k, int64_t K) {
+  if (k >= K) return lu4{0u, 0u, 0u, 0u};
+  lu4 u = *reinterpret_cast<const lu4*>(row + k);
+  if (k + 8 > K) {
+    for (int j = 0; j < 4; ++j)
+      u[j] &= (k + 2 * j < K ? 0xFFFFu : 0u) | (k + 2 * j + 1 < K ? 0xFFFF0000u : 0u);
+  }
+  return u;
+}
+
+template <typename T, int NB>
+__global__ __launch_bounds__(kFewWaves * 64, 2) void k_linear_few(Linear a) {
+  constexpr int U = NB <= 2 ? 4 : 2;  // lines of a batch
+  __shared__ lf4 lds[kFewWaves][NB][2][64];
+  const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t c0 = blockIdx.x * kFewCols;
+  const uint16_t *aw[2], *bx[NB];
+  for (int i = 0; i < 2; ++i)
+    aw[i] = static_cast<const uint16_t*>(a.a) +
+            (int64_t)min(c0 + i * 16 + (l & 15), a.cols - 1) * a.lda;
+  for (int j = 0; j < NB; ++j)
+    bx[j] = static_cast<const uint16_t*>(a.b) +
+            min((int64_t)(j * 16 + (l & 15)), a.rows - 1) * a.ldb;
+  lf4 acc[2][NB];
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < NB; ++j) acc[i][j] = lf4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t step = kFewWaves * 64;
+  for (int64_t k0 = wave * 64; k0 < a.k; k0 += step * U) {
+    lu4 fa[U][2][2], fb[U][NB][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t k = k0 + u * step + h * 32 + (l >> 4) * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) fa[u][i][h] = load_k(aw[i], k, a.k);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) fb[u][j][h] = load_k(bx[j], k, a.k);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            acc[i][j] = mfma(fa[u][i][h], fb[u][j][h], acc[i][j], (const T*)nullptr);
+  }
+  for (int j = 0; j < NB; ++j)
+    for (int i = 0; i < 2; ++i) lds[wave][j][i][l] = acc[i][j];
+  __syncthreads();
+  if (wave >= NB) return;
+  // wave j finishes rows 16j .. 16j+15: four lanes to a row, eight columns each
+  const int row = l >> 2, cc = (l & 3) * 8;
+  const int64_t r = wave * 16 + row;
+  const int32_t c = c0 + cc;
+  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, b[8];
+  Extra x;
+  load_bias(a, c, b);
+  load_extra<LinearKind::kForward>(a, r, c, x);
+  for (int w = 0; w < kFewWaves; ++w)
+    for (int h = 0; h < 2; ++h) {
+      const lf4 p = lds[w][wave][cc / 16][((cc % 16) / 4 + h) * 16 + row];
+      for (int j = 0; j < 4; ++j) v[4 * h + j] += p[j];
+    }
+  finish<T, LinearKind::kForward>(a, r, c, b, x, v);
 }
 
 // ---- joining a split product ------------------------------------------------------
@@ -482,7 +599,11 @@ __global__ __launch_bounds__(256) void k_linear_join(Linear a, int32_t splits) {
       store_bias_grad(a, worker, r, s);
     }
   } else {
-    finish<T, KIND>(a, true, wr, c, v);
+    float b[8];
+    Extra x;
+    if constexpr (KIND == LinearKind::kForward) load_bias(a, c, b);
+    load_extra<KIND>(a, wr, c, x);
+    finish<T, KIND>(a, wr, c, b, x, v);
   }
 }
 
@@ -514,15 +635,35 @@ Choice choose(int32_t n, int64_t rows, int32_t cols, int64_t k) {
   return c;
 }
 
+// Whether the few-rows kernel takes a forward product: one launch and no
+// workspace, but cols / 32 blocks that each walk all of k, a batch of lines at
+// a time.  Against the split tiles (us, with the 5 us of the timing events):
+// 16 x 1600 -> 6400 10.4 and 16.4, 64 x 1600 -> 6400 15.8 and 18.9, 1 x 4096
+// -> 1024 13.2 and 16.3; but 64 x 4096 -> 1024 27.8 and 18.5, 1 x 16384 -> 1024
+// 40.6 and 33.2.  With a block for every CU a long k does no harm.
+bool few(LinearKind kind, int64_t rows, int32_t cols, int64_t k) {
+  if (kind != LinearKind::kForward || rows > 64) return false;
+  return (k <= 4096 && rows * k <= 131072) || cols >= kCUs * kFewCols;
+}
+
+template <typename T>
+void product_few(const Linear& a, hipStream_t st) {
+  const dim3 grid((a.cols + kFewCols - 1) / kFewCols), block(kFewWaves * 64);
+  if (a.rows <= 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_few<T, 1>), grid, block, 0, st, a);
+  else if (a.rows <= 32)
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_few<T, 2>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_few<T, 4>), grid, block, 0, st, a);
+}
+
 template <typename T, LinearKind KIND>
 void product(const Linear& a, hipStream_t st) {
   const Choice c = choose(a.n, a.rows, a.cols, a.k);
   const uint32_t grid = (uint32_t)((int64_t)c.t.ta * c.t.tb * c.t.splits * a.n);
   if (c.big)
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear<T, KIND, 256, 256, 2, 4>), dim3(grid), dim3(512),
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear<T, KIND, 256, 256, 2, 4, 2>), dim3(grid), dim3(512),
                        0, st, a, c.t);
   else
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear<T, KIND, 128, 128, 2, 2>), dim3(grid), dim3(256),
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear<T, KIND, 128, 128, 2, 2, 2>), dim3(grid), dim3(256),
                        0, st, a, c.t);
 }
 
@@ -536,7 +677,8 @@ void join(const Linear& a, hipStream_t st) {
 
 template <typename T>
 void product(LinearKind kind, const Linear& a, hipStream_t st) {
-  if (kind == LinearKind::kForward) product<T, LinearKind::kForward>(a, st);
+  if (few(kind, a.rows, a.cols, a.k)) product_few<T>(a, st);
+  else if (kind == LinearKind::kForward) product<T, LinearKind::kForward>(a, st);
   else if (kind == LinearKind::kInputGrad) product<T, LinearKind::kInputGrad>(a, st);
   else product<T, LinearKind::kWeightGrad>(a, st);
 }
@@ -550,7 +692,8 @@ void join(LinearKind kind, const Linear& a, hipStream_t st) {
 
 }  // namespace
 
-int32_t linear_splits(LinearKind, int32_t n, int64_t rows, int32_t cols, int64_t k) {
+int32_t linear_splits(LinearKind kind, int32_t n, int64_t rows, int32_t cols, int64_t k) {
+  if (few(kind, rows, cols, k)) return 1;
   return choose(n, rows, cols, k).t.splits;
 }
 

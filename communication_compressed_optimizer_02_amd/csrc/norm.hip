@@ -8,8 +8,8 @@
 // and, per worker and column, dgamma = sum dy * xhat, dbeta = sum dy.
 // Everything is bound by the rows' bytes: a row is read once into registers.
 //
-// A row belongs to one wave up to 2048 columns, to a block of 4 waves up to
-// 8192 and of 8 waves up to 16384.  A wave walks many rows, so that gamma
+// A row belongs to one wave up to 1024 columns, to a block of 4 waves up to
+// 4096 and of 8 waves up to 16384.  A wave walks many rows, so that gamma
 // and beta are read once and, in the backward pass, the column sums stay in
 // binary32 registers until the wave's last row; blocks write them as partial
 // sums, which a second kernel adds per column in binary64 in a fixed order.
@@ -31,11 +31,6 @@ template <typename T, int W>
 __device__ __forceinline__ int32_t chunk_col(int c) {
   const int32_t t = W == 1 ? (int32_t)(threadIdx.x & 63) : (int32_t)threadIdx.x;
   return (c * W * 64 + t) * kVec<T>;
-}
-
-__device__ __forceinline__ float wave_sum32(float v) {
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
-  return v;
 }
 
 // Sums of two values over the waves of a row; every lane gets them.  `lds`
@@ -61,6 +56,9 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* lds) {
 
 // Columns from a binary32 vector of any alignment (parameters live anywhere
 // in the flat x); those past cols read as 0.
+struct __attribute__((packed, aligned(4))) Four {
+  float v[4];
+};
 template <typename T, int NC, int W>
 __device__ __forceinline__ void load_params(const float* __restrict__ p, int32_t cols,
                                             float (&v)[NC][kVec<T>]) {
@@ -68,30 +66,60 @@ __device__ __forceinline__ void load_params(const float* __restrict__ p, int32_t
   for (int c = 0; c < NC; ++c) {
     const int32_t col = chunk_col<T, W>(c);
 #pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) v[c][j] = col + j < cols ? p[col + j] : 0.0f;
+    for (int j = 0; j < kVec<T>; j += 4) {
+      if (col + j + 4 <= cols) {
+        const Four f = *reinterpret_cast<const Four*>(p + col + j);
+        for (int i = 0; i < 4; ++i) v[c][j + i] = f.v[i];
+      } else {
+        for (int i = 0; i < 4; ++i) v[c][j + i] = col + j + i < cols ? p[col + j + i] : 0.0f;
+      }
+    }
   }
 }
 
+// The waves of a block: 4 rows at a time with a wave each, or one row.
+template <int W>
+constexpr int kThreads = W == 1 ? 256 : W * 64;
+template <int W>
+constexpr int kRows = W == 1 ? 4 : 1;
+
+// Waves per SIMD asked of the compiler: what the registers of a row of NC
+// pieces allow without spilling.
+template <typename T, int NC>
+constexpr int kFwdWaves = NC * kVec<T> <= 16 ? 4 : 2;
+template <typename T, int NC>
+constexpr int kBwdWaves = NC * kVec<T> <= 8 ? 4 : NC * kVec<T> <= 16 ? 3 : 2;
+
 template <typename T, int NC, int W, bool KEEP>
-__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_norm_fwd(
+__global__ __launch_bounds__((kThreads<W>), (kFwdWaves<T, NC>)) void k_norm_fwd(
     int64_t rows, int32_t cols, const T* __restrict__ x, int64_t ldx,
     const float* __restrict__ gamma, const float* __restrict__ beta, float eta,
     T* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd,
     uint8_t* __restrict__ q, uint8_t* __restrict__ e) {
-  constexpr int V = kVec<T>, R = W == 1 ? 4 : 1;  // rows a block works on at a time
+  constexpr int V = kVec<T>, R = kRows<W>;
   __shared__ float lds[2 * W];
   const int32_t groups = (cols + kAct8Group - 1) / kAct8Group;
+  const int64_t stride = (int64_t)gridDim.x * R;
+  int64_t r = (int64_t)blockIdx.x * R + (W == 1 ? threadIdx.x >> 6 : 0);
+  // a row ahead: its loads are in flight while this one is worked on
+  lu4 next[NC];
+  if (r < rows) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) next[c] = load_raw(x + r * ldx, chunk_col<T, W>(c), cols);
+  }
   float ga[NC][V], be[NC][V];
   load_params<T, NC, W>(gamma, cols, ga);
   load_params<T, NC, W>(beta, cols, be);
   const float n = (float)cols;
-  for (int64_t r = (int64_t)blockIdx.x * R + (W == 1 ? threadIdx.x >> 6 : 0); r < rows;
-       r += (int64_t)gridDim.x * R) {
+  for (; r < rows; r += stride) {
     float v[NC][V];
     float s = 0.0f, z = 0.0f;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      load_row(x + r * ldx, chunk_col<T, W>(c), cols, v[c]);
+    for (int c = 0; c < NC; ++c) unpack_row<T>(next[c], chunk_col<T, W>(c), cols, v[c]);
+    if (r + stride < rows) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        next[c] = load_raw(x + (r + stride) * ldx, chunk_col<T, W>(c), cols);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -129,18 +157,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_norm_fwd(
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) top = max(top, magnitude(v[c][j]));
-#pragma unroll
-        for (int m = 1; m < kAct8Group / V; m <<= 1)
-          top = max(top, (uint32_t)__shfl_xor((int)top, m));
+        top = max_lanes<kAct8Group / V>(top);
         const uint32_t ex = group_exp(top);
-        const float inv = inv_step_of(ex);
+        const float inv = inv_step_of(ex), step = step_of(ex);
         if (col < groups * kAct8Group) {  // a started group is written whole
           uint8_t* at = q + r * (int64_t)groups * kAct8Group + col;
           if constexpr (V == 8)
             *reinterpret_cast<lu2*>(at) =
-                lu2{quant4(v[c], inv, ex != 255u), quant4(v[c] + 4, inv, ex != 255u)};
+                lu2{quant4(v[c], inv, step, ex != 255u), quant4(v[c] + 4, inv, step, ex != 255u)};
           else
-            *reinterpret_cast<uint32_t*>(at) = quant4(v[c], inv, ex != 255u);
+            *reinterpret_cast<uint32_t*>(at) = quant4(v[c], inv, step, ex != 255u);
           if (col % kAct8Group == 0) e[r * groups + col / kAct8Group] = (uint8_t)ex;
         }
       }
@@ -149,13 +175,63 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_norm_fwd(
 }
 
 // ---- backward ------------------------------------------------------------------
+// What a row's backward pass reads, as it lies in memory.
+template <typename T, int NC, bool KEPT>
+struct BwdRow {
+  lu4 dy[NC], add[NC];
+  lu4 x[KEPT ? 1 : NC];
+  lu2 q[KEPT ? NC : 1];
+  uint32_t e[KEPT ? NC : 1];
+  float rs, mu;
+};
+
 template <typename T, int NC, int W, bool KEPT>
-__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_norm_bwd(NormBwd a) {
-  constexpr int V = kVec<T>, R = W == 1 ? 4 : 1;
+__device__ __forceinline__ void load_bwd(const NormBwd& a, int64_t r, int32_t groups,
+                                         BwdRow<T, NC, KEPT>& w) {
+  w.rs = a.rstd[r];
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    w.dy[c] = load_raw(static_cast<const T*>(a.dy) + r * a.lddy, chunk_col<T, W>(c), a.cols);
+  if constexpr (KEPT) {
+    const uint8_t* qr = reinterpret_cast<const uint8_t*>(a.q) + r * (int64_t)groups * kAct8Group;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int32_t col = chunk_col<T, W>(c);
+      w.q[c] = lu2{0u, 0u};
+      w.e[c] = 0u;
+      if (col < a.cols) {
+        if constexpr (kVec<T> == 8) w.q[c] = *reinterpret_cast<const lu2*>(qr + col);
+        else w.q[c][0] = *reinterpret_cast<const uint32_t*>(qr + col);
+        w.e[c] = a.e[r * groups + col / kAct8Group];
+      }
+    }
+  } else {
+    w.mu = a.mean[r];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      w.x[c] = load_raw(static_cast<const T*>(a.x) + r * a.ldx, chunk_col<T, W>(c), a.cols);
+  }
+  if (a.add) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      w.add[c] = load_raw(static_cast<const T*>(a.add) + r * a.ldadd, chunk_col<T, W>(c), a.cols);
+  }
+}
+
+template <typename T, int NC, int W, bool KEPT>
+__global__ __launch_bounds__((kThreads<W>), (kBwdWaves<T, NC>)) void k_norm_bwd(NormBwd a) {
+  constexpr int V = kVec<T>, R = kRows<W>;
   __shared__ float lds[2 * W];
   const int32_t cols = a.cols, groups = (cols + kAct8Group - 1) / kAct8Group;
   const int32_t worker = blockIdx.y;
-  const int64_t base = (int64_t)worker * a.rows;
+  const int64_t base = (int64_t)worker * a.rows, stride = (int64_t)gridDim.x * R;
+  int64_t i = (int64_t)blockIdx.x * R + (W == 1 ? threadIdx.x >> 6 : 0);
+  // a row ahead where that leaves the registers for as many waves (at 16
+  // columns a lane it cost a wave or spilled: 65 or 57 us against 50 for
+  // 32768 x 1024 in bfloat16)
+  constexpr bool kAhead = NC * V <= 8;
+  BwdRow<T, NC, KEPT> next;
+  if (kAhead && i < a.rows) load_bwd<T, NC, W, KEPT>(a, base + i, groups, next);
   float ga[NC][V], dg[NC][V], db[NC][V];
   load_params<T, NC, W>(a.gamma, cols, ga);
 #pragma unroll
@@ -163,44 +239,34 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_norm_bwd(NormBwd a) {
 #pragma unroll
     for (int j = 0; j < V; ++j) dg[c][j] = db[c][j] = 0.0f;
   const float n = (float)cols;
-  for (int64_t i = (int64_t)blockIdx.x * R + (W == 1 ? threadIdx.x >> 6 : 0); i < a.rows;
-       i += (int64_t)gridDim.x * R) {
+  for (; i < a.rows; i += stride) {
     const int64_t r = base + i;
+    if (!kAhead) load_bwd<T, NC, W, KEPT>(a, r, groups, next);
     float h[NC][V], d[NC][V];
-    const float rs = a.rstd[r];
+    lu4 add[NC];
+    const float rs = next.rs, mu = next.mu;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-      load_row(static_cast<const T*>(a.dy) + r * a.lddy, chunk_col<T, W>(c), cols, d[c]);
-    if constexpr (KEPT) {
-      const uint8_t* qr = reinterpret_cast<const uint8_t*>(a.q) + r * (int64_t)groups * kAct8Group;
+    for (int c = 0; c < NC; ++c) {
+      const int32_t col = chunk_col<T, W>(c);
+      unpack_row<T>(next.dy[c], col, cols, d[c]);
+      add[c] = next.add[c];
+      if constexpr (KEPT) {
+        const float step = step_of(next.e[c]);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int32_t col = chunk_col<T, W>(c);
-        lu2 u = {0u, 0u};
-        float step = 0.0f;
-        if (col < cols) {
-          if constexpr (V == 8) u = *reinterpret_cast<const lu2*>(qr + col);
-          else u[0] = *reinterpret_cast<const uint32_t*>(qr + col);
-          step = step_of(a.e[r * groups + col / kAct8Group]);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[c][j] = dequant(u[j / 4], j % 4, step);
+        for (int j = 0; j < V; ++j) h[c][j] = dequant(next.q[c][j / 4], j % 4, step);
+      } else {
+        unpack_row<T>(next.x[c], col, cols, h[c]);
       }
-    } else {
-      const float mu = a.mean[r];
+    }
+    if (kAhead && i + stride < a.rows) load_bwd<T, NC, W, KEPT>(a, r + stride, groups, next);
+    float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        load_row(static_cast<const T*>(a.x) + r * a.ldx, chunk_col<T, W>(c), cols, h[c]);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int32_t col = chunk_col<T, W>(c);
+    for (int c = 0; c < NC; ++c) {
+      const int32_t col = chunk_col<T, W>(c);
+      if constexpr (!KEPT) {
 #pragma unroll
         for (int j = 0; j < V; ++j) h[c][j] = col + j < cols ? (h[c][j] - mu) * rs : 0.0f;
       }
-    }
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float t = d[c][j] * ga[c][j];
@@ -210,13 +276,14 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_norm_bwd(NormBwd a) {
         s2 += t * h[c][j];
         d[c][j] = t;
       }
+    }
     row_sum2<W>(s1, s2, lds);
     const float m1 = s1 / n, m2 = s2 / n;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
       float o[V];
-      if (a.add) load_row(static_cast<const T*>(a.add) + r * a.ldadd, col, cols, o);
+      if (a.add) unpack(add[c], o, (const T*)nullptr);
       else
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] = 0.0f;
@@ -261,36 +328,42 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void k_norm_bwd(NormBwd a) {
 }
 
 // Column sums of a worker from its blocks' partial sums, in binary64: 64
-// columns to a block, 4 waves that each add every fourth partial, joined in
+// columns to a block of 16 waves that each add every 16th partial, joined in
 // wave order.
+constexpr int kJoinWaves = 16;
 template <typename G>
-__global__ __launch_bounds__(256) void k_norm_wgrad(const float* __restrict__ part,
-                                                    int32_t blocks, int32_t cols,
-                                                    G* __restrict__ dgamma,
-                                                    G* __restrict__ dbeta, int64_t ldg) {
-  __shared__ double lds[4][64];
-  const int32_t col = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+__global__ __launch_bounds__(kJoinWaves * 64) void k_norm_wgrad(const float* __restrict__ part,
+                                                                int32_t blocks, int32_t cols,
+                                                                G* __restrict__ dgamma,
+                                                                G* __restrict__ dbeta,
+                                                                int64_t ldg) {
+  __shared__ double lds[kJoinWaves][64];
+  const int32_t l = threadIdx.x & 63, w = threadIdx.x >> 6, col = blockIdx.x * 64 + l;
   const float* p = part + (int64_t)blockIdx.y * blocks * 2 * cols;
   double s = 0.0;
-  if (col < 2 * cols)
-    for (int32_t b = w; b < blocks; b += 4) s += p[(int64_t)b * 2 * cols + col];
-  lds[w][threadIdx.x & 63] = s;
+  if (col < 2 * cols) {
+#pragma unroll 4
+    for (int32_t b = w; b < blocks; b += kJoinWaves) s += p[(int64_t)b * 2 * cols + col];
+  }
+  lds[w][l] = s;
   __syncthreads();
   if (w == 0 && col < 2 * cols) {
-    const int l = threadIdx.x;
-    const float t = (float)(((lds[0][l] + lds[1][l]) + lds[2][l]) + lds[3][l]);
-    if (col < cols) dgamma[(int64_t)blockIdx.y * ldg + col] = (G)t;
-    else dbeta[(int64_t)blockIdx.y * ldg + col - cols] = (G)t;
+    s = 0.0;
+    for (int v = 0; v < kJoinWaves; ++v) s += lds[v][l];
+    if (col < cols) dgamma[(int64_t)blockIdx.y * ldg + col] = (G)(float)s;
+    else dbeta[(int64_t)blockIdx.y * ldg + col - cols] = (G)(float)s;
   }
 }
 
 // ---- launchers -------------------------------------------------------------------
 template <typename T, int NC, int W>
 void fwd_keep(const NormFwd& a, hipStream_t st) {
-  constexpr int R = W == 1 ? 4 : 1;
-  const int64_t want = (a.rows + R - 1) / R;
-  const uint32_t grid = (uint32_t)std::min<int64_t>(want, W == 1 ? 2048 : W == 4 ? 2048 : 512);
-  const dim3 block(W == 1 ? 256 : W * 64);
+  // one round of resident blocks: kFwdWaves waves on each of the 4 SIMDs of
+  // 256 CUs, and no more than there are rows for
+  const int64_t want = (a.rows + kRows<W> - 1) / kRows<W>;
+  const int64_t most = 256 * 256 * kFwdWaves<T, NC> / kThreads<W>;
+  const uint32_t grid = (uint32_t)std::min(want, most);
+  const dim3 block(kThreads<W>);
   auto* q = reinterpret_cast<uint8_t*>(a.q);
   if (a.q)
     hipLaunchKernelGGL(HIP_KERNEL_NAME(k_norm_fwd<T, NC, W, true>), dim3(grid), block, 0, st,
@@ -302,22 +375,21 @@ void fwd_keep(const NormFwd& a, hipStream_t st) {
                        static_cast<T*>(a.y), a.ldy, a.mean, a.rstd, q, a.e);
 }
 
-// The smallest instance that holds a row; M = 1 for 16-byte pieces of eight
-// elements, 2 for binary32's four.
+// The instance that holds a row.  Binary32 rows take twice the pieces (M).
 template <typename T>
 void fwd(const NormFwd& a, hipStream_t st) {
   constexpr int M = 8 / kVec<T>;
   if (a.cols <= 512) fwd_keep<T, M, 1>(a, st);
   else if (a.cols <= 1024) fwd_keep<T, 2 * M, 1>(a, st);
-  else if (a.cols <= 2048) fwd_keep<T, 4 * M, 1>(a, st);
+  else if (a.cols <= 2048) fwd_keep<T, M, 4>(a, st);
   else if (a.cols <= 4096) fwd_keep<T, 2 * M, 4>(a, st);
-  else if (a.cols <= 8192) fwd_keep<T, 4 * M, 4>(a, st);
+  else if (a.cols <= 8192) fwd_keep<T, 2 * M, 8>(a, st);
   else fwd_keep<T, 4 * M, 8>(a, st);
 }
 
 template <typename T, int NC, int W>
 void bwd_kept(const NormBwd& a, hipStream_t st) {
-  const dim3 grid(norm_bwd_blocks(a.n, a.rows, a.cols), a.n), block(W == 1 ? 256 : W * 64);
+  const dim3 grid(norm_bwd_blocks(a.n, a.rows, a.cols), a.n), block(kThreads<W>);
   if (a.q) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_norm_bwd<T, NC, W, true>), grid, block, 0, st, a);
   else hipLaunchKernelGGL(HIP_KERNEL_NAME(k_norm_bwd<T, NC, W, false>), grid, block, 0, st, a);
 }
@@ -327,26 +399,28 @@ void bwd(const NormBwd& a, hipStream_t st) {
   constexpr int M = 8 / kVec<T>;
   if (a.cols <= 512) bwd_kept<T, M, 1>(a, st);
   else if (a.cols <= 1024) bwd_kept<T, 2 * M, 1>(a, st);
-  else if (a.cols <= 2048) bwd_kept<T, 4 * M, 1>(a, st);
+  else if (a.cols <= 2048) bwd_kept<T, M, 4>(a, st);
   else if (a.cols <= 4096) bwd_kept<T, 2 * M, 4>(a, st);
-  else if (a.cols <= 8192) bwd_kept<T, 4 * M, 4>(a, st);
+  else if (a.cols <= 8192) bwd_kept<T, 2 * M, 8>(a, st);
   else bwd_kept<T, 4 * M, 8>(a, st);
 }
 
 template <typename G>
 void wgrad(const NormBwd& a, hipStream_t st) {
   hipLaunchKernelGGL(HIP_KERNEL_NAME(k_norm_wgrad<G>), dim3((2 * a.cols + 63) / 64, a.n),
-                     dim3(256), 0, st, a.part, a.rows ? norm_bwd_blocks(a.n, a.rows, a.cols) : 0,
+                     dim3(kJoinWaves * 64), 0, st, a.part, a.rows ? norm_bwd_blocks(a.n, a.rows, a.cols) : 0,
                      a.cols, static_cast<G*>(a.dgamma), static_cast<G*>(a.dbeta), a.ldg);
 }
 
 }  // namespace
 
-// About four blocks to a CU over all workers, and no more than a worker has
-// rows for.
+// One round of resident blocks over all workers (kBwdWaves waves a SIMD), and
+// no more than a worker has rows for.
 int32_t norm_bwd_blocks(int32_t n, int64_t rows, int32_t cols) {
-  const int64_t per = cols <= 2048 ? 4 : 1;
-  const int64_t most = std::max<int64_t>(1, (cols <= 8192 ? 1024 : 512) / n);
+  const int64_t per = cols <= 1024 ? 4 : 1;  // rows of a block at a time
+  const int64_t all = cols <= 512 ? 1024 : cols <= 1024 ? 768 : cols <= 2048 ? 1024
+                      : cols <= 4096 ? 768 : 256;
+  const int64_t most = std::max<int64_t>(1, all / n);
   return (int32_t)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, most));
 }
 
