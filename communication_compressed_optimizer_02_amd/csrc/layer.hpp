@@ -50,14 +50,16 @@ __device__ __forceinline__ void unpack(const lu4 u, float (&v)[8], const __bf16*
   }
 }
 
-// Two binary32 values rounded to T (nearest, ties to even), packed.
+// Two binary32 values rounded to T (nearest, ties to even), packed by one
+// instruction.
+typedef float lf2 __attribute__((ext_vector_type(2)));
+typedef _Float16 lh2 __attribute__((ext_vector_type(2)));
+typedef __bf16 lb2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pack2(float a, float b, const _Float16*) {
-  return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |
-         (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(lf2{a, b}, lh2));
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b, const __bf16*) {
-  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) |
-         (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(lf2{a, b}, lb2));
 }
 __device__ __forceinline__ lu4 pack(const float (&v)[4], const float*) {
   lu4 u;
@@ -145,6 +147,19 @@ __device__ __forceinline__ float wave_sum32(float v) {
 // ---- kept activations ------------------------------------------------------
 __device__ __forceinline__ uint32_t magnitude(float x) {
   return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
+}
+
+// The largest magnitude bits of eight values.  As signed integers the largest
+// is the largest positive value, as unsigned ones the most negative value if
+// there is one: two three-way maxima for two values, and no masking of signs.
+__device__ __forceinline__ uint32_t magnitude8(const float (&v)[8]) {
+  int32_t p = 0;
+  uint32_t m = 0;
+  for (int j = 0; j < 8; ++j) {
+    p = max(p, __builtin_bit_cast(int32_t, v[j]));
+    m = max(m, __builtin_bit_cast(uint32_t, v[j]));
+  }
+  return max((uint32_t)p, m > 0x80000000u ? m & 0x7FFFFFFFu : 0u);
 }
 
 // The exponent byte of a group with largest magnitude bits `top`: the step is

@@ -58,20 +58,38 @@ __device__ __forceinline__ uint32_t krow_at(uint32_t row, uint32_t piece) {
   return row * 128u + ((piece ^ (row & 7u)) << 4);
 }
 template <int R>
-__device__ __forceinline__ uint32_t kcol_at(uint32_t k, uint32_t block) {
+__device__ __forceinline__ uint32_t kcol_block(uint32_t k, uint32_t block) {
   const uint32_t f = (k & 3u) | ((k >> 3) & 3u) << 2;
-  return k * (R * 2u) + (((block ^ f) & (R / 16 - 1)) << 5);
+  return (block ^ f) & (R / 16 - 1);
+}
+template <int R>
+__device__ __forceinline__ uint32_t kcol_at(uint32_t k, uint32_t block) {
+  return k * (R * 2u) + (kcol_block<R>(k, block) << 5);
 }
 
-// One thread's share of an operand's tile: its pieces of 8 elements on the
-// way from memory to LDS.  `off` are element offsets from the tile's origin,
-// rows past the operand's end read its last row (results there are not
+// One thread's share of an operand's tile: pieces of 8 elements, each with a
+// place of 16 bytes in LDS, places in the order of threads, so that a wave's
+// 64 are one kilobyte: what the direct load from memory to LDS writes.  The
+// permutation is therefore in the address that a place is loaded from.
+// Rows past the operand's end read its last row (results there are not
 // stored).
 template <typename T, int SRC, int R, int NT>
 struct Stage {
   static constexpr int P = R * (kBK / 8) / NT;
-  lu4 reg[P];
-  uint32_t off[P], eoff[P];
+  static constexpr int kBytes = SRC == kKept ? 1 : 2;  // of an element in memory
+  uint32_t off[P];   // bytes from the tile's origin
+  uint32_t eoff[SRC == kKept ? P : 1];
+  lu2 reg[SRC == kKept ? P : 1];  // kKept: a step's integers and exponents in flight
+  uint32_t exp[SRC == kKept ? P : 1];
+
+  // the k of piece p, from the step's first
+  __device__ __forceinline__ static int32_t k_of(int p) {
+    const uint32_t i = p * NT + threadIdx.x;
+    if constexpr (SRC == kKRow)
+      return (int32_t)((i % (kBK / 8)) ^ (i / (kBK / 8) & 7u)) * 8;
+    else
+      return (int32_t)(i / (R / 8));
+  }
 
   // r0: first row of the tile, of `rows`; ld, eld: strides in elements
   __device__ __forceinline__ void init(int32_t r0, int32_t rows, uint32_t ld, uint32_t eld) {
@@ -79,64 +97,79 @@ struct Stage {
     for (int p = 0; p < P; ++p) {
       const uint32_t i = p * NT + threadIdx.x;
       if constexpr (SRC == kKRow) {
-        const uint32_t r = i / (kBK / 8), c = i % (kBK / 8);
-        off[p] = min(r, (uint32_t)(rows - 1 - r0)) * ld + c * 8;
+        off[p] = (min(i / (kBK / 8), (uint32_t)(rows - 1 - r0)) * ld + (uint32_t)k_of(p)) * 2;
       } else {
         const uint32_t k = i / (R / 8), c = i % (R / 8);
-        const uint32_t col = min(c * 8, (uint32_t)(rows - 1 - r0) & ~7u);
-        off[p] = k * ld + col;
+        const uint32_t block = kcol_block<R>(k, c / 2);
+        const uint32_t col = min(block * 16 + (c & 1) * 8, (uint32_t)(rows - 1 - r0) & ~7u);
+        off[p] = (k * ld + col) * kBytes;
         if constexpr (SRC == kKept) eoff[p] = k * eld + col / kAct8Group;
       }
     }
   }
 
-  // left: elements along k from this step to the end of the sum; a step of
-  // fewer than kBK reads nothing past the end and gives zeros there
+  // A whole step straight to LDS (16-bit operands): a buffer at the step's
+  // origin, so that a lane's offsets never change.
+  __device__ __forceinline__ void direct(const char* base, char* lds) const {
+#if defined(__HIP_DEVICE_COMPILE__)  // the buffer type exists on the device only
+    typedef __attribute__((address_space(3))) uint32_t* lp;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, -1, 0x00027000);
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          r, (lp)(lds + (p * NT + wave * 64) * 16), 16, off[p], 0, 0, 0);
+#endif
+  }
+
+  // kKept: a step's elements to registers; at or past `left` they are 0.
   template <bool TAIL>
-  __device__ __forceinline__ void load(const void* __restrict__ base,
-                                       const uint8_t* __restrict__ ebase, int32_t left,
-                                       uint32_t ld, uint32_t eld) {
+  __device__ __forceinline__ void load(const char* base, const uint8_t* ebase, int32_t left) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const uint32_t i = p * NT + threadIdx.x;
-      const int32_t k = SRC == kKRow ? (int32_t)(i % (kBK / 8)) * 8 : (int32_t)(i / (R / 8));
-      if (TAIL && k >= left) {
-        reg[p] = lu4{0u, 0u, 0u, 0u};
-        continue;
-      }
-      if constexpr (SRC == kKept) {
-        const lu2 q = *reinterpret_cast<const lu2*>(static_cast<const uint8_t*>(base) + off[p]);
-        reg[p] = lu4{q[0], q[1], (uint32_t)ebase[eoff[p]], 0u};
+      if (!TAIL || k_of(p) < left) {
+        reg[p] = *reinterpret_cast<const lu2*>(base + off[p]);
+        exp[p] = ebase[eoff[p]];
       } else {
-        reg[p] = *reinterpret_cast<const lu4*>(static_cast<const T*>(base) + off[p]);
-        if (TAIL && SRC == kKRow && k + 8 > left) {
-          for (int j = 0; j < 4; ++j)
-            reg[p][j] &= (k + 2 * j < left ? 0xFFFFu : 0u) |
-                         (k + 2 * j + 1 < left ? 0xFFFF0000u : 0u);
-        }
+        reg[p] = lu2{0u, 0u};
+        exp[p] = 0u;
       }
     }
   }
-
-  __device__ __forceinline__ void store(char* __restrict__ lds) const {
+  // An integer of at most 7 bits times a power of two: exact in T but for
+  // binary16's range, which rows encoded from binary16 do not leave.
+  __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const uint32_t i = p * NT + threadIdx.x;
-      lu4 u = reg[p];
-      if constexpr (SRC == kKept) {
-        // an integer of at most 7 bits times a power of two: exact in T but
-        // for binary16's range, which rows encoded from binary16 do not leave
-        const float s = step_of(reg[p][2]);
-        float v[8];
-        for (int j = 0; j < 8; ++j) v[j] = dequant(reg[p][j / 4], j % 4, s);
-        u = pack(v, (const T*)nullptr);
+      const float s = step_of(exp[p]);
+      float v[8];
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w = reg[p][h];
+        // kept whole until here: the compiler took the bytes apart when they
+        // were loaded and carried 32 registers from step to step
+        asm("" : "+v"(w));
+        for (int j = 0; j < 4; ++j) v[4 * h + j] = dequant(w, j, s);
       }
-      if constexpr (SRC == kKRow) {
-        *reinterpret_cast<lu4*>(lds + krow_at(i / (kBK / 8), i % (kBK / 8))) = u;
-      } else {
-        const uint32_t c = i % (R / 8);
-        *reinterpret_cast<lu4*>(lds + kcol_at<R>(i / (R / 8), c / 2) + (c & 1) * 16) = u;
+      *reinterpret_cast<lu4*>(lds + (p * NT + threadIdx.x) * 16) = pack(v, (const T*)nullptr);
+    }
+  }
+
+  // The last step of a sum that is no multiple of kBK: through registers, the
+  // elements past its end 0 (16-bit operands).
+  __device__ __forceinline__ void tail(const char* base, char* lds, int32_t left) const {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int32_t k = k_of(p);
+      lu4 u = {0u, 0u, 0u, 0u};
+      if (k < left) {
+        u = *reinterpret_cast<const lu4*>(base + off[p]);
+        if (SRC == kKRow && k + 8 > left) {
+          for (int j = 0; j < 4; ++j)
+            u[j] &= (k + 2 * j < left ? 0xFFFFu : 0u) | (k + 2 * j + 1 < left ? 0xFFFF0000u : 0u);
+        }
       }
+      *reinterpret_cast<lu4*>(lds + (p * NT + threadIdx.x) * 16) = u;
     }
   }
 };
@@ -214,21 +247,18 @@ __device__ __forceinline__ void finish(const Linear& a, int64_t r, int32_t c, co
   if constexpr (KIND == LinearKind::kForward) {
     if (a.bias)
       for (int j = 0; j < 8; ++j) v[j] += b[j];
-    if (a.q) {  // columns past the last are kept as 0
+    if (a.q) {
       const int32_t groups = (a.cols + kAct8Group - 1) / kAct8Group;
-      uint32_t top = 0;
-      float w[8];
-      for (int j = 0; j < 8; ++j) {
-        w[j] = j < n ? v[j] : 0.0f;
-        top = max(top, magnitude(w[j]));
+      if (n < 8) {  // columns past the last are kept as 0
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? v[j] : 0.0f;
       }
-      top = max_lanes<4>(top);
+      const uint32_t top = max_lanes<4>(magnitude8(v));
       const uint32_t ex = group_exp(top);
       const float inv = inv_step_of(ex), step = step_of(ex);
       if (in_rows && c / kAct8Group < groups) {
         const int64_t g = r * groups + c / kAct8Group;
         *reinterpret_cast<lu2*>(a.q + g * kAct8Group + c % kAct8Group) =
-            lu2{quant4(w, inv, step, ex != 255u), quant4(w + 4, inv, step, ex != 255u)};
+            lu2{quant4(v, inv, step, ex != 255u), quant4(v + 4, inv, step, ex != 255u)};
         if (c % kAct8Group == 0) a.e[g] = (uint8_t)ex;
       }
     }
@@ -305,15 +335,15 @@ __device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
   return x * q + min(x, r) + i;
 }
 
-template <typename T, LinearKind KIND, int BA, int BB, int WA, int WB, int BUFS>
-__global__ __launch_bounds__(WA* WB * 64, 2) void k_linear(Linear a, Tiles t) {
+template <typename T, LinearKind KIND, int BA, int BB, int WA, int WB>
+__global__ __launch_bounds__(WA* WB * 64, 3) void k_linear(Linear a, Tiles t) {
   constexpr int NT = WA * WB * 64;
   constexpr int ASRC = KIND == LinearKind::kForward ? kKRow
                        : KIND == LinearKind::kInputGrad ? kKCol : kKept;
   constexpr int BSRC = KIND == LinearKind::kWeightGrad ? kKCol : kKRow;
   constexpr int TA = BA / WA / 16, TB = BB / WB / 16;
-  constexpr int kStageBytes = (BA + BB) * kBK * 2;
-  __shared__ __align__(1024) char lds[BUFS * kStageBytes];
+  constexpr int kA = BA * kBK * 2, kStageBytes = kA + BB * kBK * 2;  // of a step in LDS
+  __shared__ __align__(1024) char lds[kStageBytes];
 
   const int64_t work = xcd_order(blockIdx.x, gridDim.x);
   const int32_t tiles = t.ta * t.tb;
@@ -356,7 +386,8 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void k_linear(Linear a, Tiles t) {
   sa.init(c0, a.cols, (uint32_t)a.lda, eld);
   sb.init(r0, (int32_t)min(a.rows, (int64_t)0x7FFFFFFF), (uint32_t)a.ldb, 0);
 
-  const int wave = threadIdx.x >> 6, wa = wave % WA, wb = wave / WA;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // uniform
+  const int wa = wave % WA, wb = wave / WA;
   lf4 acc[TA][TB];
 #pragma unroll
   for (int i = 0; i < TA; ++i)
@@ -370,51 +401,78 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void k_linear(Linear a, Tiles t) {
   const uint32_t one2 = pack2(1.0f, 1.0f, (const T*)nullptr);
   const lu4 one8 = {one2, one2, one2, one2};
 
-  auto load = [&](int64_t k) {
-    const int64_t left = kend - k;
-    if (left >= kBK) {
-      sa.template load<false>(ap, ae, kBK, (uint32_t)a.lda, eld);
-      sb.template load<false>(bp, nullptr, kBK, (uint32_t)a.ldb, 0);
-    } else {
-      sa.template load<true>(ap, ae, (int32_t)left, (uint32_t)a.lda, eld);
-      sb.template load<true>(bp, nullptr, (int32_t)left, (uint32_t)a.ldb, 0);
+  // the direct loads of a wave have landed in LDS (a barrier alone does not
+  // wait for them)
+  auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
+  auto direct = [&](char* l) __attribute__((always_inline)) {
+    if constexpr (ASRC != kKept) {
+      sa.direct(ap, l);
+      ap += astep;
     }
-    ap += astep;
+    sb.direct(bp, l + kA);
     bp += bstep;
-    if constexpr (ASRC == kKept) ae += (int64_t)kBK * eld;
+  };
+  // the kept operand's step to registers: a whole one, or the sum's last
+  auto load_full = [&]() __attribute__((always_inline)) {
+    if constexpr (ASRC == kKept) {
+      sa.template load<false>(ap, ae, kBK);
+      ap += astep;
+      ae += (int64_t)kBK * eld;
+    }
+  };
+  auto load_tail = [&](int32_t left) __attribute__((always_inline)) {
+    if constexpr (ASRC == kKept) sa.template load<true>(ap, ae, left);
+  };
+  auto products = [&](const lu4 (&fa)[TA], const lu4 (&fb)[TB]) {
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+#pragma unroll
+      for (int i = 0; i < TA; ++i) acc[i][j] = mfma(fa[i], fb[j], acc[i][j], (const T*)nullptr);
+    if constexpr (KIND == LinearKind::kWeightGrad) {
+      if (ones) {
+#pragma unroll
+        for (int j = 0; j < TB; ++j) accb[j] = mfma(one8, fb[j], accb[j], (const T*)nullptr);
+      }
+    }
+  };
+  auto fragments = [&](const char* la, const char* lb, int ks, lu4 (&fa)[TA], lu4 (&fb)[TB]) {
+#pragma unroll
+    for (int i = 0; i < TA; ++i) fa[i] = fragment<ASRC, BA>(la, (wa * TA + i) * 16, ks);
+#pragma unroll
+    for (int j = 0; j < TB; ++j) fb[j] = fragment<BSRC, BB>(lb, (wb * TB + j) * 16, ks);
   };
 
-  if (kbeg < kend) load(kbeg);
-  int buf = 0;
-  for (int64_t k = kbeg; k < kend; k += kBK) {
-    char* la = lds + buf * kStageBytes;
-    char* lb = la + BA * kBK * 2;
-    sa.store(la);
-    sb.store(lb);
-    // a barrier a step: the other half is written only after every wave has
-    // passed the next one, and so has read this half
-    __syncthreads();
-    if (k + kBK < kend) load(k + kBK);
+  auto compute = [&](const char* l) __attribute__((always_inline)) {
 #pragma unroll
     for (int ks = 0; ks < kBK / 32; ++ks) {
       lu4 fa[TA], fb[TB];
-#pragma unroll
-      for (int i = 0; i < TA; ++i) fa[i] = fragment<ASRC, BA>(la, (wa * TA + i) * 16, ks);
-#pragma unroll
-      for (int j = 0; j < TB; ++j) fb[j] = fragment<BSRC, BB>(lb, (wb * TB + j) * 16, ks);
-#pragma unroll
-      for (int j = 0; j < TB; ++j)
-#pragma unroll
-        for (int i = 0; i < TA; ++i) acc[i][j] = mfma(fa[i], fb[j], acc[i][j], (const T*)nullptr);
-      if constexpr (KIND == LinearKind::kWeightGrad) {
-        if (ones) {
-#pragma unroll
-          for (int j = 0; j < TB; ++j) accb[j] = mfma(one8, fb[j], accb[j], (const T*)nullptr);
-        }
-      }
+      fragments(l, l + kA, ks, fa, fb);
+      products(fa, fb);
     }
-    if constexpr (BUFS == 1) __syncthreads();  // all have read before the next is written
-    else buf ^= 1;
+  };
+  const int32_t full = (int32_t)((kend - kbeg) / kBK), rest_k = (int32_t)((kend - kbeg) % kBK);
+  auto load_rest = [&]() __attribute__((always_inline)) {
+    if (rest_k > 0) load_tail(rest_k);
+  };
+  if (full > 0) load_full();
+  else load_rest();
+  for (int32_t s = 0; s < full; ++s) {
+    if (s > 0) __syncthreads();  // every wave is done with the last step's tile
+    direct(lds);
+    if constexpr (ASRC == kKept) sa.store(lds);
+    if (s + 1 < full) load_full();
+    else load_rest();
+    landed();
+    __syncthreads();
+    compute(lds);
+  }
+  if (rest_k > 0) {
+    if (full > 0) __syncthreads();
+    if constexpr (ASRC == kKept) sa.store(lds);
+    else sa.tail(ap, lds, rest_k);
+    sb.tail(bp, lds + kA, rest_k);
+    __syncthreads();
+    compute(lds);
   }
 
   // The results go through LDS, 16 rows of a wave at a time and within the
@@ -423,7 +481,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void k_linear(Linear a, Tiles t) {
   // are whole lines.
   constexpr int kRow = TA * 16 + 4;  // floats of a row in LDS, off the bank period
   constexpr int kLanes = TA * 2;     // lanes of a row
-  static_assert(WA * WB * 16 * kRow * 4 <= BUFS * kStageBytes, "epilogue rows fit the stages");
+  static_assert(WA * WB * 16 * kRow * 4 <= kStageBytes, "epilogue rows fit the tile");
   const int l = threadIdx.x & 63;
   float* rows = reinterpret_cast<float*>(lds) + wave * 16 * kRow;
   const bool vec = KIND == LinearKind::kWeightGrad && grad_vec(a);
@@ -609,30 +667,19 @@ __global__ __launch_bounds__(256) void k_linear_join(Linear a, int32_t splits) {
 
 // ---- host side ----------------------------------------------------------------------
 constexpr int kCUs = 256;
+constexpr int kTile = 128;
 
-struct Choice {
-  bool big;
+Tiles choose(int32_t n, int64_t rows, int32_t cols, int64_t k) {
   Tiles t;
-};
-
-int64_t tiles_of(int64_t rows, int64_t cols, int tile) {
-  return ((rows + tile - 1) / tile) * ((cols + tile - 1) / tile);
-}
-
-Choice choose(int32_t n, int64_t rows, int32_t cols, int64_t k) {
-  Choice c;
-  c.big = tiles_of(rows, cols, 256) * n >= kCUs * 3 / 4;
-  const int tile = c.big ? 256 : 128;
-  c.t.ta = (int32_t)((cols + tile - 1) / tile);
-  c.t.tb = (int32_t)((rows + tile - 1) / tile);
-  const int64_t all = tiles_of(rows, cols, tile) * n, steps = (k + kBK - 1) / kBK;
+  t.ta = (int32_t)((cols + kTile - 1) / kTile);
+  t.tb = (int32_t)((rows + kTile - 1) / kTile);
+  const int64_t all = (int64_t)t.ta * t.tb * n, steps = (k + kBK - 1) / kBK;
   int64_t splits = 1;
   // a product of few tiles: up to two blocks to a CU, at least four steps each
-  if (!c.big && all <= kCUs)
-    splits = std::max<int64_t>(1, std::min<int64_t>(2 * kCUs / all, steps / 4));
-  c.t.ksteps = (int32_t)std::max<int64_t>(1, (steps + splits - 1) / splits);
-  c.t.splits = (int32_t)std::max<int64_t>(1, (steps + c.t.ksteps - 1) / c.t.ksteps);
-  return c;
+  if (all <= kCUs) splits = std::max<int64_t>(1, std::min<int64_t>(2 * kCUs / all, steps / 4));
+  t.ksteps = (int32_t)std::max<int64_t>(1, (steps + splits - 1) / splits);
+  t.splits = (int32_t)std::max<int64_t>(1, (steps + t.ksteps - 1) / t.ksteps);
+  return t;
 }
 
 // Whether the few-rows kernel takes a forward product: one launch and no
@@ -657,22 +704,18 @@ void product_few(const Linear& a, hipStream_t st) {
 
 template <typename T, LinearKind KIND>
 void product(const Linear& a, hipStream_t st) {
-  const Choice c = choose(a.n, a.rows, a.cols, a.k);
-  const uint32_t grid = (uint32_t)((int64_t)c.t.ta * c.t.tb * c.t.splits * a.n);
-  if (c.big)
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear<T, KIND, 256, 256, 2, 4, 2>), dim3(grid), dim3(512),
-                       0, st, a, c.t);
-  else
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear<T, KIND, 128, 128, 2, 2, 2>), dim3(grid), dim3(256),
-                       0, st, a, c.t);
+  const Tiles t = choose(a.n, a.rows, a.cols, a.k);
+  const uint32_t grid = (uint32_t)((int64_t)t.ta * t.tb * t.splits * a.n);
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear<T, KIND, kTile, kTile, 2, 2>), dim3(grid), dim3(256),
+                     0, st, a, t);
 }
 
 template <typename T, LinearKind KIND>
 void join(const Linear& a, hipStream_t st) {
-  const Choice c = choose(a.n, a.rows, a.cols, a.k);
+  const Tiles t = choose(a.n, a.rows, a.cols, a.k);
   const int64_t lanes = (int64_t)a.n * a.rows * ((a.cols + kAct8Group - 1) / kAct8Group) * 4;
   hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_join<T, KIND>), dim3((uint32_t)((lanes + 255) / 256)),
-                     dim3(256), 0, st, a, c.t.splits);
+                     dim3(256), 0, st, a, t.splits);
 }
 
 template <typename T>
@@ -694,7 +737,7 @@ void join(LinearKind kind, const Linear& a, hipStream_t st) {
 
 int32_t linear_splits(LinearKind kind, int32_t n, int64_t rows, int32_t cols, int64_t k) {
   if (few(kind, rows, cols, k)) return 1;
-  return choose(n, rows, cols, k).t.splits;
+  return choose(n, rows, cols, k).splits;
 }
 
 size_t linear_workspace(LinearKind kind, int32_t n, int64_t rows, int32_t cols, int64_t k) {
