@@ -14,8 +14,10 @@ from .binding import (OBA_BF16, OBA_F16, OBA_F32, Layout, ObaError, Plateau, Sta
                       linear_weight_grad, linear_weight_grad_workspace, linear_workspace,
                       server_momentum, server_reduce_recompress,
                       server_reduce_recompress_deferred, step_small, timing_enable, timing_read, timing_reset, validate)
+from .feedforward import FeedForward
 
 __all__ = [
+    "FeedForward",
     "OBA_BF16", "OBA_F16", "OBA_F32", "Layout", "ObaError", "Plateau", "State", "TensorList",
     "adam_warmup_step", "adam_warmup_step_listed", "compress_deferred_listed",
     "decompress_update_listed",
