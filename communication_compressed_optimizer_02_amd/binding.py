@@ -567,28 +567,30 @@ def step_small(L: Layout, g, m, c, wbits, wscale, a, sbits, sscale, denom, m_out
 
 ACT8_GROUP = 32
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3}
-_TYPES = None  # torch dtype -> OBA code (filled at the first call: torch is imported late)
+_TYPES = {}     # torch dtype -> OBA code
+_torch_module = None
 
 
-def _types():
-    global _TYPES
-    if _TYPES is None:
+def _torch():
+    """torch, imported at the first layer call."""
+    global _torch_module
+    if _torch_module is None:
         import torch
 
-        _TYPES = {torch.float32: OBA_F32, torch.float16: OBA_F16, torch.bfloat16: OBA_BF16}
-    return _TYPES
+        _TYPES.update({torch.float32: OBA_F32, torch.float16: OBA_F16, torch.bfloat16: OBA_BF16})
+        _torch_module = torch
+    return _torch_module
 
 
 class _Call:
-    """Argument checks of one layer call: every tensor on the current device."""
+    """Argument checks of one layer call: every tensor on the current device.
+    Kept short: a small call's kernel takes 3 us, its launch as much."""
 
     __slots__ = ("torch", "dev")
 
     def __init__(self):
-        import torch
-
-        self.torch = torch
-        self.dev = torch.cuda.current_device()
+        self.torch = _torch()
+        self.dev = self.torch.cuda.current_device()
 
     def stream(self, stream):
         return self.torch.cuda.current_stream(self.dev).cuda_stream if stream is None \
@@ -604,12 +606,13 @@ class _Call:
         """(pointer, row stride) of a matrix; the shape and the type are
         checked where they are given."""
         self._on(t, name)
-        if t.dim() != 2:
+        shape = t.shape
+        if len(shape) != 2:
             raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
-        r, c = t.shape
+        r, c = shape
         if (rows is not None and r != rows) or (cols is not None and c != cols):
             raise ValueError(f"{name}: shape {tuple(t.shape)} != {(rows, cols)}")
-        if t.dtype not in _types() or (dtype is not None and t.dtype != dtype):
+        if t.dtype not in _TYPES or (dtype is not None and t.dtype != dtype):
             raise TypeError(f"{name}: dtype {t.dtype}" +
                             (f" != {dtype}" if dtype is not None else " not supported"))
         ld, one = t.stride()
@@ -625,10 +628,11 @@ class _Call:
                              "(columns rounded up to 8)")
         return t.data_ptr(), ld
 
-    def vec(self, t, name, dtype, size):
+    def vec(self, t, name, size):
+        """Pointer of a float32 vector."""
         self._on(t, name)
-        if t.dtype != dtype:
-            raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
+        if t.dtype != self.torch.float32:
+            raise TypeError(f"{name}: dtype {t.dtype} != torch.float32")
         if t.numel() != size or not t.is_contiguous():
             raise ValueError(f"{name}: expected {size} contiguous elements, got {tuple(t.shape)}")
         return t.data_ptr()
@@ -653,7 +657,7 @@ class _Call:
         """(type, stride, pointers) of parameter tensors' places (offset or
         None, length) in the gradient rows g [n][ld]."""
         self._on(g, "g")
-        if g.dtype not in _types():
+        if g.dtype not in _TYPES:
             raise TypeError(f"g: dtype {g.dtype} not supported")
         if g.dim() != 2 or g.shape[0] != n or not g.is_contiguous():
             raise ValueError(f"g: expected {n} contiguous rows, got {tuple(g.shape)}")
@@ -669,7 +673,7 @@ class _Call:
                 raise ValueError("g: two gradients overlap")
             taken.append((at, at + length))
             out.append(base + at * size)
-        return _types()[g.dtype], ld, out
+        return _TYPES[g.dtype], ld, out
 
     def ws(self, ws):
         if ws is None:
@@ -700,7 +704,7 @@ def act8_encode(x, q, e, stream=None):
     c = _Call()
     xp, ldx = c.rows(x, "x")
     qp, ep = c.kept(q, e, *x.shape)
-    _check(lib().oba_act8_encode(*x.shape, xp, ldx, _types()[x.dtype], qp, ep, c.stream(stream)),
+    _check(lib().oba_act8_encode(*x.shape, xp, ldx, _TYPES[x.dtype], qp, ep, c.stream(stream)),
            "oba_act8_encode")
 
 
@@ -709,7 +713,7 @@ def act8_decode(q, e, x, stream=None):
     c = _Call()
     xp, ldx = c.rows(x, "x")
     qp, ep = c.kept(q, e, *x.shape)
-    _check(lib().oba_act8_decode(*x.shape, qp, ep, xp, ldx, _types()[x.dtype], c.stream(stream)),
+    _check(lib().oba_act8_decode(*x.shape, qp, ep, xp, ldx, _TYPES[x.dtype], c.stream(stream)),
            "oba_act8_decode")
 
 
@@ -717,15 +721,14 @@ def layer_norm(x, gamma, beta, eta, y, mean, rstd, q=None, e=None, stream=None):
     """y = xhat * gamma + beta; mean and rstd [rows] float32 are written; with
     (q, e) xhat is kept in 8 bits."""
     c = _Call()
-    f32 = c.torch.float32
     rows, cols = x.shape
     xp, ldx = c.rows(x, "x")
     yp, ldy = c.rows(y, "y", rows, cols, x.dtype)
     qp, ep = c.kept(q, e, rows, cols)
-    _check(lib().oba_layer_norm(rows, cols, xp, ldx, _types()[x.dtype],
-                                c.vec(gamma, "gamma", f32, cols), c.vec(beta, "beta", f32, cols),
-                                eta, yp, ldy, c.vec(mean, "mean", f32, rows),
-                                c.vec(rstd, "rstd", f32, rows), qp, ep, c.stream(stream)),
+    _check(lib().oba_layer_norm(rows, cols, xp, ldx, _TYPES[x.dtype],
+                                c.vec(gamma, "gamma", cols), c.vec(beta, "beta", cols),
+                                eta, yp, ldy, c.vec(mean, "mean", rows),
+                                c.vec(rstd, "rstd", rows), qp, ep, c.stream(stream)),
            "oba_layer_norm")
 
 
@@ -740,7 +743,6 @@ def layer_norm_backward(n, dy, gamma, rstd, dx, g, at_gamma, at_beta, ws, x=None
     its row of g [n][ld].  The normalised rows come from (x, mean) or from
     (q, e); add: the gradient that goes round the layer, or None."""
     c = _Call()
-    f32 = c.torch.float32
     dyp, lddy = c.rows(dy, "dy")
     total, cols = dy.shape
     if n < 1 or total % n:
@@ -752,9 +754,9 @@ def layer_norm_backward(n, dy, gamma, rstd, dx, g, at_gamma, at_beta, ws, x=None
     gt, ldg, (gp, bp) = c.grads(g, n, (at_gamma, cols), (at_beta, cols))
     wp, wb = c.ws(ws)
     _check(lib().oba_layer_norm_backward(
-        n, total // n, cols, dyp, lddy, _types()[dy.dtype], xp, ldx,
-        c.vec(mean, "mean", f32, total) if mean is not None else None, qp, ep,
-        c.vec(rstd, "rstd", f32, total), c.vec(gamma, "gamma", f32, cols), ap, lda, dxp, lddx,
+        n, total // n, cols, dyp, lddy, _TYPES[dy.dtype], xp, ldx,
+        c.vec(mean, "mean", total) if mean is not None else None, qp, ep,
+        c.vec(rstd, "rstd", total), c.vec(gamma, "gamma", cols), ap, lda, dxp, lddx,
         gp, bp, gt, ldg, wp, wb, c.stream(stream)), "oba_layer_norm_backward")
 
 
@@ -777,8 +779,8 @@ def linear(x, w, y, ws, bias=None, act="none", residual=None, q=None, e=None, st
     qp, ep = c.kept(q, e, rows, n_out)
     sp, sb = c.ws(ws)
     _check(lib().oba_linear(
-        rows, n_in, n_out, xp, ldx, wp, ldw, _types()[x.dtype],
-        c.vec(bias, "bias", c.torch.float32, n_out) if bias is not None else None, ACTS[act],
+        rows, n_in, n_out, xp, ldx, wp, ldw, _TYPES[x.dtype],
+        c.vec(bias, "bias", n_out) if bias is not None else None, ACTS[act],
         rp, ldr, yp, ldy, qp, ep, sp, sb, c.stream(stream)), "oba_linear")
 
 
@@ -794,7 +796,7 @@ def linear_input_grad(dy, w, dx, ws, act="none", q=None, e=None, add=None, strea
     qp, ep = c.kept(q, e, rows, n_in)
     sp, sb = c.ws(ws)
     _check(lib().oba_linear_input_grad(
-        rows, n_in, n_out, dyp, lddy, wp, ldw, _types()[dy.dtype], ACTS[act], qp, ep, ap, lda,
+        rows, n_in, n_out, dyp, lddy, wp, ldw, _TYPES[dy.dtype], ACTS[act], qp, ep, ap, lda,
         dxp, lddx, sp, sb, c.stream(stream)), "oba_linear_input_grad")
 
 
@@ -817,7 +819,7 @@ def linear_weight_grad(n, dy, q, e, g, n_in, at_w, at_bias, ws, stream=None):
     gt, ldg, (gp, bp) = c.grads(g, n, (at_w, n_in * n_out), (at_bias, n_out))
     sp, sb = c.ws(ws)
     _check(lib().oba_linear_weight_grad(
-        n, total // n, n_in, n_out, dyp, lddy, _types()[dy.dtype], qp, ep, gp, bp, gt, ldg, sp,
+        n, total // n, n_in, n_out, dyp, lddy, _TYPES[dy.dtype], qp, ep, gp, bp, gt, ldg, sp,
         sb, c.stream(stream)), "oba_linear_weight_grad")
 
 

@@ -624,6 +624,8 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void k_linear_few(Linear a) {
   finish<T, LinearKind::kForward>(a, r, c, b, x, v);
 }
 
+constexpr int kMaxSplits = 8;
+
 // ---- joining a split product ------------------------------------------------------
 // A thread adds eight columns' sums in split order and finishes them as above;
 // four lanes hold a group of 32 columns.
@@ -637,14 +639,21 @@ __global__ __launch_bounds__(256) void k_linear_join(Linear a, int32_t splits) {
   if (wr >= all) return;  // whole groups of lanes
   float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (c < a.cols) {
-    for (int32_t s = 0; s < splits; ++s) {
-      const lf4* p = reinterpret_cast<const lf4*>(a.part + ((int64_t)s * all + wr) * pc + c);
-      const lf4 x = p[0], y = p[1];
-      for (int j = 0; j < 4; ++j) {
-        v[j] += x[j];
-        v[4 + j] += y[j];
+    lf4 x[kMaxSplits], y[kMaxSplits];
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s)  // all loads before the first sum
+      if (s < splits) {
+        const lf4* p = reinterpret_cast<const lf4*>(a.part + ((int64_t)s * all + wr) * pc + c);
+        x[s] = p[0];
+        y[s] = p[1];
       }
-    }
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s)
+      if (s < splits)
+        for (int j = 0; j < 4; ++j) {
+          v[j] += x[s][j];
+          v[4 + j] += y[s][j];
+        }
   }
   if constexpr (KIND == LinearKind::kWeightGrad) {
     const int32_t worker = (int32_t)(wr / a.rows);
@@ -675,8 +684,13 @@ Tiles choose(int32_t n, int64_t rows, int32_t cols, int64_t k) {
   t.tb = (int32_t)((rows + kTile - 1) / kTile);
   const int64_t all = (int64_t)t.ta * t.tb * n, steps = (k + kBK - 1) / kBK;
   int64_t splits = 1;
-  // a product of few tiles: up to two blocks to a CU, at least four steps each
-  if (all <= kCUs) splits = std::max<int64_t>(1, std::min<int64_t>(2 * kCUs / all, steps / 4));
+  // A product of few tiles: up to two blocks to a CU, at least four steps
+  // each, and at most kMaxSplits sums to join (us, 256 x 4096 -> 1024: 16
+  // splits 26.4, 8 splits 22.2; 515 x 1000 -> 776: 4 splits 17.7, 2 splits
+  // 20.5, none 28.3).
+  if (all <= kCUs)
+    splits = std::max<int64_t>(
+        1, std::min<int64_t>({2 * kCUs / all, steps / 4, (int64_t)kMaxSplits}));
   t.ksteps = (int32_t)std::max<int64_t>(1, (steps + splits - 1) / splits);
   t.splits = (int32_t)std::max<int64_t>(1, (steps + t.ksteps - 1) / t.ksteps);
   return t;

@@ -1,10 +1,15 @@
 """Refusals of the layer operators: argument errors are found on the host,
-before any HIP call, so made-up addresses serve and nothing is launched."""
+before any HIP call, so made-up addresses serve and nothing is launched.  They
+run where there is no GPU: a refusal that is missing ends in a failed launch."""
 import ctypes
+import os
 
 import pytest
 
 from communication_compressed_optimizer_02_amd import binding as oba
+
+pytestmark = pytest.mark.skipif(os.path.exists("/dev/kfd"),
+                                reason="made-up addresses: not where a GPU could read them")
 
 EINVAL, EALIGN, EWORKSPACE = -1, -2, -4
 F32, F16, BF16 = 0, 1, 2
@@ -28,7 +33,7 @@ NORM = dict(rows=4, cols=40, x=A, ldx=40, dtype=BF16, gamma=A, beta=A, eta=1e-5,
 NORM_B = dict(n=2, rows=4, cols=40, dy=A, lddy=40, dtype=BF16, x=A, ldx=40, mean=A, q=None,
               e=None, rstd=A, gamma=A, add=None, ldadd=0, dx=A, lddx=40, dgamma=A, dbeta=A,
               g_dtype=F16, ldg=80, ws=A, ws_bytes=1 << 20, stream=None)
-LINEAR = dict(rows=4, n_in=2048, n_out=64, x=A, ldx=2048, w=A, ldw=2048, dtype=BF16, bias=A, act=2,
+LINEAR = dict(rows=100, n_in=2048, n_out=64, x=A, ldx=2048, w=A, ldw=2048, dtype=BF16, bias=A, act=2,
               residual=A, ldr=64, y=A, ldy=64, q=A, e=A, ws=A, ws_bytes=1 << 24, stream=None)
 INPUT = dict(rows=4, n_in=64, n_out=2048, dy=A, lddy=2048, w=A, ldw=64, dtype=F16, act=2, q=A,
              e=A, add=A, ldadd=64, dx=A, lddx=64, ws=A, ws_bytes=1 << 24, stream=None)
