@@ -120,7 +120,7 @@ def test_workspace_sizes():
     """The workspace holds what a call needs: one product of few tiles is
     split, a large one is not, and sizes that are refused need none."""
     L = oba.lib()
-    assert L.oba_linear_workspace_bytes(1, 2048, 64) > 0
+    assert L.oba_linear_workspace_bytes(100, 2048, 64) > 0
     assert L.oba_linear_workspace_bytes(16384, 1024, 4096) == 0
     assert L.oba_linear_workspace_bytes(0, 64, 64) == 0
     assert L.oba_linear_workspace_bytes(-1, 64, 64) == 0
