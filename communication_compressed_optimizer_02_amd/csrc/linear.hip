@@ -688,7 +688,7 @@ Tiles choose(int32_t n, int64_t rows, int32_t cols, int64_t k) {
   // each, and at most kMaxSplits sums to join (us, 256 x 4096 -> 1024: 16
   // splits 26.4, 8 splits 22.2; 515 x 1000 -> 776: 4 splits 17.7, 2 splits
   // 20.5, none 28.3).
-  if (all <= kCUs)
+  if (all > 0 && all <= kCUs)
     splits = std::max<int64_t>(
         1, std::min<int64_t>({2 * kCUs / all, steps / 4, (int64_t)kMaxSplits}));
   t.ksteps = (int32_t)std::max<int64_t>(1, (steps + splits - 1) / splits);
