@@ -18,6 +18,21 @@
 //           way to LDS
 // Sums are binary32 in the accumulators, in increasing k; a product of few
 // tiles is split over k, its binary32 sums joined in split order.
+//
+// One 128 x 128 tile serves all three: a step of 64 along k is 32 KB, loaded
+// straight to LDS (no registers, no LDS writes by the waves), so that three
+// blocks of four waves fit a CU and one's products hide the others' loads and
+// epilogues.  At 16384 x 1024 -> 4096 in bfloat16 (137 GFLOP; us): 148 bare,
+// 180 with GELU, 186-198 with GELU and the pre-activation kept, 145 the input
+// gradient, 200 with GELU's derivative from 8 bits, 171 the weight gradients
+// of 8 workers from 8 bits; the library's bare product takes 106.  A 256 x 256
+// tile of eight waves with two halves of LDS took 152 bare, but 208 with its
+// epilogue, which nothing hides; 128 x 256 took 140, 168 and 197, and 216 for
+// the input gradient with GELU's derivative.  What bounds it: at K = 1024 the
+// epilogue's vector instructions (about 36 a result with GELU kept) are as
+// long as the products; at K = 4096 the products run at 1.1 PFLOP/s, where LDS
+// is the nearest limit (64 KB of fragments and 32 KB of loads for 512 cycles
+// of products).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -551,7 +566,9 @@ __global__ __launch_bounds__(WA* WB * 64, 3) void k_linear(Linear a, Tiles t) {
 // of the 8-bit form); its 8 waves share k in lines of 64, each wave's
 // fragments straight from memory (a line of w is used by one wave, once), all
 // of a batch's loads before its products.  The waves' sums meet in LDS, added
-// in wave order.
+// in wave order.  1 x 1600 -> 6400 (20 MB of w): 7.4 us, 2.8 TB/s, bound by the
+// loads' latency (two batches a wave) and 200 blocks for 256 CUs; split tiles
+// and their join took 9.0 + 5.0.
 constexpr int kFewWaves = 8, kFewCols = 32;
 
 // The 8 elements of a row from k; those at or past K are 0.
@@ -684,13 +701,18 @@ Tiles choose(int32_t n, int64_t rows, int32_t cols, int64_t k) {
   t.tb = (int32_t)((rows + kTile - 1) / kTile);
   const int64_t all = (int64_t)t.ta * t.tb * n, steps = (k + kBK - 1) / kBK;
   int64_t splits = 1;
-  // A product of few tiles: up to two blocks to a CU, at least four steps
-  // each, and at most kMaxSplits sums to join (us, 256 x 4096 -> 1024: 16
-  // splits 26.4, 8 splits 22.2; 515 x 1000 -> 776: 4 splits 17.7, 2 splits
-  // 20.5, none 28.3).
-  if (all > 0 && all <= kCUs)
+  // A product of few tiles: up to two blocks to a CU, at most kMaxSplits sums
+  // to join, and at least four steps each, ten where the tiles alone give half
+  // the CUs a block: the join moves each sum twice.  In us, with 5 of the
+  // timing events: 256 x 4096 -> 1024 16 splits 26.4, 8 splits 21.3; 515 x 1000
+  // -> 776 4 splits 17.7, 2 splits 20.5, none 28.3; 256 x 512 -> 512 2 splits
+  // 12.6, none 15.2; 1024 x 1024 -> 3200 2 splits 32.9, none 25.2; 640 x 2048
+  // -> 4096 2 splits 34.2, none 41.5.
+  if (all > 0 && all <= kCUs) {
+    const int64_t least = all <= kCUs / 2 ? 4 : 10;
     splits = std::max<int64_t>(
-        1, std::min<int64_t>({2 * kCUs / all, steps / 4, (int64_t)kMaxSplits}));
+        1, std::min<int64_t>({2 * kCUs / all, steps / least, (int64_t)kMaxSplits}));
+  }
   t.ksteps = (int32_t)std::max<int64_t>(1, (steps + splits - 1) / splits);
   t.splits = (int32_t)std::max<int64_t>(1, (steps + t.ksteps - 1) / t.ksteps);
   return t;
