@@ -34,6 +34,7 @@ class FeedForward:
             raise ValueError(f"act: {act!r} is none of {sorted(oba.ACTS)}")
         self.width, self.hidden, self.n, self.rows = width, hidden, n, rows
         self.act, self.eta = act, eta
+        self.flat = None  # the parameters that load() was given
         self.dtype = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
         # the parameters' places in the flat vector, from `at`
         self.places, pos = {}, at
@@ -84,7 +85,10 @@ class FeedForward:
         self.w2.copy_(self.part(flat, "w2").view(self.width, self.hidden))
 
     def forward(self, x):
+        """y, in a buffer of the instance that the next forward() overwrites."""
         p = self.flat
+        if p is None:
+            raise RuntimeError("load() the parameters first")
         oba.layer_norm(x, self.part(p, "gamma"), self.part(p, "beta"), self.eta, self.z,
                        self.mean, self.rstd, *self.kept_norm)
         oba.act8_encode(self.z, *self.kept_z)
@@ -96,7 +100,8 @@ class FeedForward:
         return self.y
 
     def backward(self, dy, g):
-        """dx, and every worker's gradients in its row of g [n][ld]."""
+        """dx (in a buffer of the instance), and every worker's gradients in its
+        row of g [n][ld]."""
         at = {name: place[0] for name, place in self.places.items()}
         pre = (None, None) if self.act == "none" else self.kept_pre
         oba.linear_weight_grad(self.n, dy, *self.kept_h, g, self.hidden, at["w2"], at["b2"],

@@ -278,6 +278,8 @@ def test_refusals_of_the_binding():
     F.forward(x)
     with pytest.raises(ValueError):
         FeedForward(40, 72, 2, 3, act="swish")
+    with pytest.raises(RuntimeError):  # no parameters yet
+        FeedForward(40, 72, 2, 3).forward(x)
     with pytest.raises(KeyError):
         oba.linear(F.z, F.w1, F.h, F.ws, act="swish")
     with pytest.raises(TypeError):
