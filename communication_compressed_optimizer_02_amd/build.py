@@ -36,7 +36,8 @@ HIP_FLAGS = [
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra"]
 # one translation unit per pass, plus the C ABI
 HIP_SOURCES = ("warmup.hip", "compress.hip", "scales.hip", "server.hip", "update.hip",
-               "small.hip", "act8.hip", "norm.hip", "linear.hip", "layer_api.hip", "api.hip")
+               "small.hip", "layer/act8.hip", "layer/norm.hip", "layer/linear.hip",
+               "layer/layer_api.hip", "api.hip")
 
 
 def hipcc() -> str:
@@ -61,7 +62,7 @@ def build(verbose: bool = False) -> str:
     run(["g++", *HOST_FLAGS, *inc, "-c", os.path.join(CSRC, "layout.cpp"), "-o", o])
     objs.append(o)
     for src in HIP_SOURCES:
-        o = os.path.join(obj_dir, src.replace(".hip", ".o"))
+        o = os.path.join(obj_dir, os.path.basename(src).replace(".hip", ".o"))
         run([hipcc(), *HIP_FLAGS, *inc, "-c", os.path.join(CSRC, src), "-o", o])
         objs.append(o)
     tmp = LIB + ".tmp"
