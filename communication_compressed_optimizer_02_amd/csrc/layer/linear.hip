@@ -8,9 +8,9 @@
 //
 // All three are C[r][c] = sum_k B(r, k) A(c, k).  The c side is the "A"
 // operand of v_mfma_f32_16x16x32, so that a lane's four results are four
-// consecutive columns of one row: 8-byte stores, and a group of 32 columns
-// for the 8-bit form is two neighbouring tiles of one wave.  What differs is
-// how an operand lies in memory:
+// consecutive columns of one row: one 16-byte write to the rows of LDS that
+// the epilogue takes back eight columns a lane, a group of 32 columns for the
+// 8-bit form in four lanes.  What differs is how an operand lies in memory:
 //   kKRow   [r][k], k contiguous: kept so in LDS and read 16 bytes per lane
 //   kKCol   [k][r], r contiguous: kept so in LDS and transposed by the
 //           ds_read_b64_tr_b16 instruction while it is read
