@@ -80,6 +80,19 @@ __device__ __forceinline__ void load_params(const float* __restrict__ p, int32_t
   }
 }
 
+// v - m, 0 stays at and past cols: lanes that hold none of the row subtract 0,
+// and elements are looked at one by one only where a row ends inside a lane.
+template <int V>
+__device__ __forceinline__ void centre(float (&v)[V], float m, int32_t col, int32_t cols) {
+  m = col < cols ? m : 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] -= m;
+  if (cols % V != 0) {  // the same for every lane
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = col + j < cols ? v[j] : 0.0f;
+  }
+}
+
 // The waves of a block: 4 rows at a time with a wave each, or one row.
 template <int W>
 constexpr int kThreads = W == 1 ? 256 : W * 64;
@@ -134,16 +147,19 @@ __global__ __launch_bounds__((kThreads<W>), (kFwdWaves<T, NC>)) void k_norm_fwd(
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
+      centre(v[c], mu, col, cols);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        v[c][j] = col + j < cols ? v[c][j] - mu : 0.0f;
         s1 += v[c][j];
         s2 += v[c][j] * v[c][j];
       }
     }
     row_sum2<W>(s1, s2, lds);
-    // what the centred values still sum to corrects the mean's rounding (a
-    // mean near 0 keeps its relative accuracy) and the variance
+    // what the centred values still sum to corrects the mean's rounding, which
+    // is of the mean's size and not of the spread's: in the mean (one near 0
+    // keeps its relative accuracy), in the variance and in the values
+    // themselves (a mean of 1000 spreads of binary32 rows left xhat 1e-3 off,
+    // constant rows not at 0)
     const float off = s1 / n;
     const float var = s2 / n - off * off;
     const float rs = 1.0f / __builtin_sqrtf((var < 0.0f ? 0.0f : var) + eta);  // NaN stays
@@ -155,6 +171,7 @@ __global__ __launch_bounds__((kThreads<W>), (kFwdWaves<T, NC>)) void k_norm_fwd(
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
       float o[V];
+      centre(v[c], off, col, cols);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         v[c][j] *= rs;
