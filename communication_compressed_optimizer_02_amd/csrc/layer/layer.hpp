@@ -257,8 +257,11 @@ __device__ __forceinline__ void activate_grad(float (&v)[8], int kind) {
     }
   } else if (kind == kActGeluTanh) {
     for (int j = 0; j < 8; ++j) {
-      const float x = v[j], s = sigmoid2(kTanhA * __builtin_fmaf(kTanhC * x, x * x, x));
-      const float d = __builtin_fmaf(6.0f * kTanhA * kTanhC * x, x, 2.0f * kTanhA);
+      const float x = v[j], xx = x * x, s = sigmoid2(kTanhA * __builtin_fmaf(kTanhC * x, xx, x));
+      // x s (1 - s) is 0 long before xx passes 2^100: d stays finite, so that
+      // their product is 0 there and not 0 * infinity
+      const float d = __builtin_fmaf(6.0f * kTanhA * kTanhC, __builtin_fminf(xx, 0x1p100f),
+                                     2.0f * kTanhA);
       v[j] = __builtin_fmaf(x * s * (1.0f - s), d, s);
     }
   } else if (kind == kActRelu) {
