@@ -198,11 +198,15 @@ __device__ __forceinline__ float dequant(uint32_t u, int j, float step) {
 // ---- activation functions ----------------------------------------------------
 constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3;
 
-// The results go to 16 bits (half a step: 2^-9 and 2^-12 of the value), so
-// the functions are evaluated to about 2^-19 of theirs with the hardware's
-// exp2 and reciprocal: the epilogue of a product computes one per result, and
-// erfcf and a correctly rounded division made GELU 94 of 241 us at 16384 x
-// 1024 -> 4096, these make it 32 of 180.
+// The results go to 16 bits (half a step: 2^-8 of the value in bfloat16, 2^-11
+// in binary16), so the functions are evaluated with the hardware's exp2 and
+// reciprocal.  Their error grows with the exponent, whose argument is rounded
+// in binary32: Phi is within (32 + 1.5 x^2) 2^-24 of its value, 2^-19 near 0
+// and 2^-17 at x = -8 (observed 2^-18); the tanh form's factor within
+// (8 + 16 |u|) 2^-24 for u < 0, 2^-15 at u = -24 (x = -8; observed 2^-17).  The
+// epilogue of a product computes one per result: erfcf and a correctly rounded
+// division made GELU 94 of 241 us at 16384 x 1024 -> 4096, these make it 32 of
+// 180.
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
 
