@@ -126,27 +126,40 @@ __global__ __launch_bounds__(kA8Block) void k_act8_decode(int64_t pieces, int32_
   }
 }
 
+constexpr int64_t kPerBlock = kA8Block * kA8Unroll;
+
+// Pieces of a row of vec elements: whole groups.
+int32_t pieces_of(int64_t cols, int vec) {
+  return (int32_t)((cols + kAct8Group - 1) / kAct8Group * (kAct8Group / vec));
+}
+
 template <typename T>
 void encode(int64_t rows, int32_t cols, const void* x, int64_t ldx, int8_t* q, uint8_t* e,
             hipStream_t st) {
-  const int32_t per_row = (cols + kAct8Group - 1) / kAct8Group * (kAct8Group / kVec<T>);
-  const int64_t pieces = rows * per_row, per = kA8Block * kA8Unroll;
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_act8_encode<T>), dim3((uint32_t)((pieces + per - 1) / per)),
-                     dim3(kA8Block), 0, st, pieces, per_row, cols, static_cast<const T*>(x), ldx,
+  const int32_t per_row = pieces_of(cols, kVec<T>);
+  const int64_t pieces = rows * per_row;
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_act8_encode<T>),
+                     dim3((uint32_t)((pieces + kPerBlock - 1) / kPerBlock)), dim3(kA8Block), 0, st,
+                     pieces, per_row, cols, static_cast<const T*>(x), ldx,
                      reinterpret_cast<uint8_t*>(q), e);
 }
 
 template <typename T>
 void decode(int64_t rows, int32_t cols, const int8_t* q, const uint8_t* e, void* x, int64_t ldx,
             hipStream_t st) {
-  const int32_t per_row = (cols + kAct8Group - 1) / kAct8Group * (kAct8Group / kVec<T>);
-  const int64_t pieces = rows * per_row, per = kA8Block * kA8Unroll;
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_act8_decode<T>), dim3((uint32_t)((pieces + per - 1) / per)),
-                     dim3(kA8Block), 0, st, pieces, per_row, cols,
+  const int32_t per_row = pieces_of(cols, kVec<T>);
+  const int64_t pieces = rows * per_row;
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_act8_decode<T>),
+                     dim3((uint32_t)((pieces + kPerBlock - 1) / kPerBlock)), dim3(kA8Block), 0, st,
+                     pieces, per_row, cols,
                      reinterpret_cast<const uint8_t*>(q), e, static_cast<T*>(x), ldx);
 }
 
 }  // namespace
+
+int64_t act8_blocks(int64_t rows, int64_t cols, int dtype) {
+  return (rows * pieces_of(cols, dtype == kGradF32 ? 4 : 8) + kPerBlock - 1) / kPerBlock;
+}
 
 void launch_act8_encode(int64_t rows, int32_t cols, const void* x, int64_t ldx, int dtype,
                         int8_t* q, uint8_t* e, hipStream_t st) {

@@ -29,8 +29,7 @@ int check_ptr(const void* p, uintptr_t align) {
 }
 
 bool sizes_ok(int64_t rows, int64_t cols, int64_t most_cols) {
-  return rows >= 0 && rows <= oba::kMaxRows && cols >= 1 && cols <= most_cols &&
-         rows * cols <= oba::kMaxElems;
+  return rows >= 0 && rows <= oba::kMaxRows && cols >= 1 && cols <= most_cols;
 }
 bool ld_ok(int64_t ld, int64_t cols) {
   return ld >= cols && ld % 8 == 0 && ld <= oba::kMaxLd;
@@ -55,6 +54,11 @@ size_t norm_ws(int32_t n, int64_t rows, int64_t cols) {
   return (size_t)n * oba::norm_bwd_blocks(n, rows, (int32_t)cols) * 2 * cols * sizeof(float);
 }
 
+// Whether one launch walks the product's tiles.
+bool blocks_ok(LinearKind kind, int32_t n, int64_t rows, int64_t cols, int64_t k) {
+  return oba::linear_blocks(kind, n, rows, (int32_t)cols, k) <= oba::kMaxLaunch;
+}
+
 // The product, and the join of its sums where it was split.
 int run_linear(const char* name, LinearKind kind, const oba::Linear& a, hipStream_t stream) {
   return launch(name, stream, [&] {
@@ -76,7 +80,8 @@ extern "C" {
 
 int oba_act8_encode(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dtype, int8_t* q,
                     uint8_t* e, hipStream_t stream) {
-  if (!is_type(dtype) || !sizes_ok(rows, cols, oba::kMaxCols) || !ld_ok(ldx, cols))
+  if (!is_type(dtype) || !sizes_ok(rows, cols, oba::kMaxCols) || !ld_ok(ldx, cols) ||
+      oba::act8_blocks(rows, cols, dtype) > oba::kMaxLaunch)
     return OBA_EINVAL;
   if (rows == 0) return OBA_OK;
   OBA_TRY(check_ptr(x, 16));
@@ -88,7 +93,8 @@ int oba_act8_encode(int64_t rows, int64_t cols, const void* x, int64_t ldx, int 
 
 int oba_act8_decode(int64_t rows, int64_t cols, const int8_t* q, const uint8_t* e, void* x,
                     int64_t ldx, int dtype, hipStream_t stream) {
-  if (!is_type(dtype) || !sizes_ok(rows, cols, oba::kMaxCols) || !ld_ok(ldx, cols))
+  if (!is_type(dtype) || !sizes_ok(rows, cols, oba::kMaxCols) || !ld_ok(ldx, cols) ||
+      oba::act8_blocks(rows, cols, dtype) > oba::kMaxLaunch)
     return OBA_EINVAL;
   if (rows == 0) return OBA_OK;
   OBA_TRY(check_kept(q, e));
@@ -175,7 +181,8 @@ int oba_linear(int64_t rows, int64_t in, int64_t out, const void* x, int64_t ldx
                size_t ws_bytes, hipStream_t stream) {
   if ((dtype != OBA_F16 && dtype != OBA_BF16) || !act_ok(act) ||
       !sizes_ok(rows, in, oba::kMaxCols) || !sizes_ok(rows, out, oba::kMaxCols) ||
-      !ld_ok(ldx, in) || !ld_ok(ldw, in) || !ld_ok(ldy, out) || (residual && !ld_ok(ldr, out)))
+      !blocks_ok(LinearKind::kForward, 1, rows, out, in) || !ld_ok(ldx, in) || !ld_ok(ldw, in) ||
+      !ld_ok(ldy, out) || (residual && !ld_ok(ldr, out)))
     return OBA_EINVAL;
   if (rows == 0) return OBA_OK;
   OBA_TRY(check_ptr(x, 16));
@@ -214,7 +221,8 @@ int oba_linear_input_grad(int64_t rows, int64_t in, int64_t out, const void* dy,
                           int64_t lddx, void* ws, size_t ws_bytes, hipStream_t stream) {
   if ((dtype != OBA_F16 && dtype != OBA_BF16) || !act_ok(act) ||
       !sizes_ok(rows, in, oba::kMaxCols) || !sizes_ok(rows, out, oba::kMaxCols) ||
-      !ld_ok(lddy, out) || !ld_ok(ldw, in) || !ld_ok(lddx, in) || (add && !ld_ok(ldadd, in)))
+      !blocks_ok(LinearKind::kInputGrad, 1, rows, in, out) || !ld_ok(lddy, out) ||
+      !ld_ok(ldw, in) || !ld_ok(lddx, in) || (add && !ld_ok(ldadd, in)))
     return OBA_EINVAL;
   if (rows == 0) return OBA_OK;
   // a derivative needs the kept pre-activation, and none is read without one
@@ -260,7 +268,8 @@ int oba_linear_weight_grad(int32_t n, int64_t rows, int64_t in, int64_t out, con
                            hipStream_t stream) {
   if ((dtype != OBA_F16 && dtype != OBA_BF16) || !is_type(g_dtype) || !workers_ok(n, rows) ||
       !sizes_ok(n * rows, in, oba::kMaxCols) || !sizes_ok(n * rows, out, oba::kMaxCols) ||
-      !sizes_ok(out * (int64_t)n, in, oba::kMaxCols) || !ld_ok(lddy, out) ||
+      !sizes_ok(out * (int64_t)n, in, oba::kMaxCols) ||
+      !blocks_ok(LinearKind::kWeightGrad, n, out, in, rows) || !ld_ok(lddy, out) ||
       (n > 1 && ldg < in * out))
     return OBA_EINVAL;
   OBA_TRY(check_ptr(dw, size_of(g_dtype)));

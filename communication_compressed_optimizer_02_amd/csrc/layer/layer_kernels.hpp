@@ -18,10 +18,13 @@ constexpr int64_t kMaxCols = 1 << 20;       // columns of a kept or linear matri
 constexpr int64_t kMaxNormCols = 16384;     // columns of a layer norm (a row stays in registers)
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr int64_t kMaxLd = 1 << 22;         // a tile's element offsets stay in 32 bits
-// pieces of 16 bytes that one launch of the encoding kernels can walk:
-// 2^31 blocks of 1024
-constexpr int64_t kMaxElems = (int64_t)1 << 42;
+// HIP takes fewer than 2^32 threads in a launch: blocks of 256 of the kernels
+// that have one for each part of their result (the norms' grids do not grow
+// with the rows)
+constexpr int64_t kMaxLaunch = ((int64_t)1 << 24) - 1;
 
+// Blocks of an encode or decode: 1024 pieces of 16 bytes of x each.
+int64_t act8_blocks(int64_t rows, int64_t cols, int dtype);
 void launch_act8_encode(int64_t rows, int32_t cols, const void* x, int64_t ldx, int dtype,
                         int8_t* q, uint8_t* e, hipStream_t st);
 void launch_act8_decode(int64_t rows, int32_t cols, const int8_t* q, const uint8_t* e, void* x,
@@ -100,6 +103,8 @@ struct Linear {
 };
 enum class LinearKind { kForward, kInputGrad, kWeightGrad };
 size_t linear_workspace(LinearKind kind, int32_t n, int64_t rows, int32_t cols, int64_t k);
+// Blocks of the product.
+int64_t linear_blocks(LinearKind kind, int32_t n, int64_t rows, int32_t cols, int64_t k);
 void launch_linear(LinearKind kind, const Linear& a, hipStream_t st);
 // Joins a split product's sums (launched after it when linear_splits > 1).
 int32_t linear_splits(LinearKind kind, int32_t n, int64_t rows, int32_t cols, int64_t k);

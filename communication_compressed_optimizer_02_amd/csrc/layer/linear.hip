@@ -741,7 +741,7 @@ void product_few(const Linear& a, hipStream_t st) {
 template <typename T, LinearKind KIND>
 void product(const Linear& a, hipStream_t st) {
   const Tiles t = choose(a.n, a.rows, a.cols, a.k);
-  const uint32_t grid = (uint32_t)((int64_t)t.ta * t.tb * t.splits * a.n);
+  const uint32_t grid = (uint32_t)linear_blocks(KIND, a.n, a.rows, a.cols, a.k);
   hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear<T, KIND, kTile, kTile, 2, 2>), dim3(grid), dim3(256),
                      0, st, a, t);
 }
@@ -774,6 +774,12 @@ void join(LinearKind kind, const Linear& a, hipStream_t st) {
 int32_t linear_splits(LinearKind kind, int32_t n, int64_t rows, int32_t cols, int64_t k) {
   if (few(kind, rows, cols, k)) return 1;
   return choose(n, rows, cols, k).splits;
+}
+
+int64_t linear_blocks(LinearKind kind, int32_t n, int64_t rows, int32_t cols, int64_t k) {
+  if (few(kind, rows, cols, k)) return (cols + kFewCols - 1) / kFewCols;
+  const Tiles t = choose(n, rows, cols, k);
+  return (int64_t)t.ta * t.tb * t.splits * n;
 }
 
 size_t linear_workspace(LinearKind kind, int32_t n, int64_t rows, int32_t cols, int64_t k) {

@@ -403,7 +403,9 @@ int oba_step_small(oba_layout layout, const void* g, int g_dtype, const float* m
  * of 8 and at least the columns, at most 2^22.  A row may be read up to its
  * columns rounded up to 8 (also the last row); what lies there does not
  * change results, and only the named columns are written.  At most 2^30 rows
- * and 2^20 columns (2^14 for a layer norm).  gamma, beta and bias are
+ * and 2^20 columns (2^14 for a layer norm), and no more than one launch can
+ * walk: 2^24 - 1 blocks, of 16 KB of x (its columns rounded up to 32) for the
+ * 8-bit calls, of 128 x 128 results for the products.  gamma, beta and bias are
  * binary32 vectors at any multiple of 4 bytes, so slices of the flat x serve.
  * With n workers, worker i's rows are [i*rows, (i+1)*rows), and its gradient
  * of a parameter tensor goes to where the tensor lies in its row of g:
