@@ -15,7 +15,8 @@ Buffers (all CUDA tensors on the layout's device, C-contiguous):
 The layer calls (act8_*, layer_norm*, linear*) take matrices as 2-D tensors
 with rows of a stride that is a multiple of 8 elements (columns adjacent),
 and activations kept in 8 bits as the pair (q, e) of act8_buffers().  Their
-tensors must be on the current device.
+tensors and the stream must be on the current device, and what a call writes
+must not overlap any other of its arguments (inputs may be the same tensor).
 """
 from __future__ import annotations
 
@@ -594,6 +595,9 @@ class _Call:
 
     def stream(self, stream):
         if stream is not None:
+            if stream.device_index != self.dev:
+                raise ValueError(f"stream: of cuda:{stream.device_index}, the current device is "
+                                 f"cuda:{self.dev}")
             return stream.cuda_stream
         # the current stream's handle without making a Stream object (1 us)
         raw = getattr(self.torch._C, "_cuda_getCurrentRawStream", None)
