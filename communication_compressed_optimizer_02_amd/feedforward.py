@@ -35,6 +35,7 @@ class FeedForward:
         self.width, self.hidden, self.n, self.rows = width, hidden, n, rows
         self.act, self.eta = act, eta
         self.flat = None  # the parameters that load() was given
+        self.kept = False  # whether a forward() has left what backward() reads
         self.dtype = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
         # the parameters' places in the flat vector, from `at`
         self.places, pos = {}, at
@@ -97,11 +98,14 @@ class FeedForward:
                    e=None if self.act == "none" else self.kept_pre[1])
         oba.act8_encode(self.h, *self.kept_h)
         oba.linear(self.h, self.w2, self.y, self.ws, bias=self.part(p, "b2"), residual=x)
+        self.kept = True
         return self.y
 
     def backward(self, dy, g):
         """dx (in a buffer of the instance), and every worker's gradients in its
         row of g [n][ld]."""
+        if not self.kept:
+            raise RuntimeError("forward() first: there is nothing kept to read")
         at = {name: place[0] for name, place in self.places.items()}
         pre = (None, None) if self.act == "none" else self.kept_pre
         oba.linear_weight_grad(self.n, dy, *self.kept_h, g, self.hidden, at["w2"], at["b2"],
