@@ -5,9 +5,14 @@
 The parameters are a range of the flat binary32 vector x of a State, the
 gradients of the n workers go to the same range of its gradient rows g, and
 what the backward pass needs is kept in 8 bits: the normalised rows, both
-products' inputs and the pre-activation, 2 bytes per row and column of width
-and of hidden where 16-bit copies take 4.  The rows of the workers follow each
-other: worker i's are [i*rows, (i+1)*rows).
+products' inputs and the pre-activation, 2 1/16 bytes per row and column of
+width and of hidden where 16-bit copies take 4.  Beside these an instance holds
+its results y and dx (4 bytes per row and column of width), rstd and the 16-bit
+copies of the weights.  The 16-bit rows that live within one pass (4 bytes per
+row and column of width and of hidden) and the workspace are scratch: the layers
+of a stack hold them once if each is made with share=, an instance of the same
+sizes.  The rows of the workers follow each other: worker
+i's are [i*rows, (i+1)*rows).
 
     F = FeedForward(width, hidden, n, rows)
     L = Layout(F.size, n, ...); S = State(L, "bf16")
@@ -19,7 +24,8 @@ other: worker i's are [i*rows, (i+1)*rows).
         S.warmup(...)  or  S.step_deferred(...)
 
 forward() keeps what the next backward() reads; x itself is read by forward()
-only.  One instance serves one stream at a time.
+only.  x and dy are not the instance's own y and dx.  One instance serves one
+stream at a time, and so do all that share scratch, in captured graphs too.
 """
 from __future__ import annotations
 
@@ -27,16 +33,22 @@ from . import binding as oba
 
 
 class FeedForward:
-    def __init__(self, width, hidden, n, rows, dtype="bf16", act="gelu", eta=1e-5, at=0):
+    def __init__(self, width, hidden, n, rows, dtype="bf16", act="gelu", eta=1e-5, at=0,
+                 share=None):
         import torch
 
         if act not in oba.ACTS:
             raise ValueError(f"act: {act!r} is none of {sorted(oba.ACTS)}")
+        sizes = (width, hidden, n, rows, {"f16": torch.float16, "bf16": torch.bfloat16}[dtype],
+                 torch.cuda.current_device())
+        if share is not None and share.sizes != sizes:
+            raise ValueError(f"share: an instance of {share.sizes}, not of {sizes}")
+        self.sizes = sizes
         self.width, self.hidden, self.n, self.rows = width, hidden, n, rows
         self.act, self.eta = act, eta
         self.flat = None  # the parameters that load() was given
         self.kept = False  # whether a forward() has left what backward() reads
-        self.dtype = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+        self.dtype = sizes[4]
         # the parameters' places in the flat vector, from `at`
         self.places, pos = {}, at
         for name, length in (("gamma", width), ("beta", width), ("w1", hidden * width),
@@ -50,15 +62,19 @@ class FeedForward:
             return torch.empty((r, (c + 7) // 8 * 8), dtype=self.dtype, device="cuda")[:, :c]
 
         self.w1, self.w2 = matrix(hidden, width), matrix(width, hidden)
-        self.z, self.h, self.y = matrix(total, width), matrix(total, hidden), matrix(total, width)
-        self.dh, self.dz, self.dx = (matrix(total, hidden), matrix(total, width),
-                                     matrix(total, width))
-        self.mean = torch.empty(total, device="cuda")
+        self.y, self.dx = matrix(total, width), matrix(total, width)
         self.rstd = torch.empty(total, device="cuda")
         self.kept_norm = oba.act8_buffers(total, width)   # xhat
         self.kept_z = oba.act8_buffers(total, width)      # the first product's input
         self.kept_pre = oba.act8_buffers(total, hidden)   # its result before act
         self.kept_h = oba.act8_buffers(total, hidden)     # the second product's input
+        if share is not None:
+            self.z, self.h, self.dz, self.dh = share.z, share.h, share.dz, share.dh
+            self.mean, self.ws = share.mean, share.ws
+            return
+        self.z, self.h = matrix(total, width), matrix(total, hidden)
+        self.dz, self.dh = matrix(total, width), matrix(total, hidden)
+        self.mean = torch.empty(total, device="cuda")
         self.ws = max((oba.linear_workspace(total, width, hidden),
                        oba.linear_workspace(total, hidden, width),
                        oba.linear_weight_grad_workspace(n, rows, width, hidden),
