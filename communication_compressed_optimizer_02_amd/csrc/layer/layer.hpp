@@ -131,7 +131,7 @@ __device__ __forceinline__ uint32_t max_lanes(uint32_t v) {
 
 // The sum of a wave's 64 lanes, in all of them: rows of 16 by exchanges, the
 // four rows' sums in order.
-__device__ __forceinline__ float wave_sum32(float v) {
+__device__ __forceinline__ float wave_sum(float v) {
   v += dppf<kXor1>(v);
   v += dppf<kXor2>(v);
   v += dppf<kHalfMirror>(v);
@@ -142,6 +142,26 @@ __device__ __forceinline__ float wave_sum32(float v) {
   s += __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));
   s += __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48));
   return s;
+}
+
+template <int CTRL>
+__device__ __forceinline__ double dppd(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 |
+                                        dpp<CTRL>((uint32_t)u));
+}
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += dppd<kXor1>(v);
+  v += dppd<kXor2>(v);
+  v += dppd<kHalfMirror>(v);
+  v += dppd<kMirror>(v);
+  return lane_of(v, 0) + lane_of(v, 16) + lane_of(v, 32) + lane_of(v, 48);
 }
 
 // ---- kept activations ------------------------------------------------------

@@ -40,8 +40,8 @@ __device__ __forceinline__ int32_t chunk_col(int c) {
 // holds 2 * W floats; the sums of the waves are added in wave order.
 template <int W>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float* lds) {
-  a = wave_sum32(a);
-  b = wave_sum32(b);
+  a = wave_sum(a);
+  b = wave_sum(b);
   if constexpr (W > 1) {
     __syncthreads();  // the last sums have been read by all
     if ((threadIdx.x & 63) == 0) {
@@ -55,6 +55,20 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* lds) {
       b += lds[W + w];
     }
   }
+}
+
+// The same for one value, and for one in binary64 (`lds` holds W doubles).
+template <int W, typename F>
+__device__ __forceinline__ F row_sum(F a, F* lds) {
+  a = wave_sum(a);
+  if constexpr (W > 1) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = a;
+    __syncthreads();
+    a = 0;
+    for (int w = 0; w < W; ++w) a += lds[w];
+  }
+  return a;
 }
 
 // Columns from a binary32 vector of any alignment (parameters live anywhere
@@ -80,13 +94,16 @@ __device__ __forceinline__ void load_params(const float* __restrict__ p, int32_t
   }
 }
 
-// v - m, 0 stays at and past cols: lanes that hold none of the row subtract 0,
-// and elements are looked at one by one only where a row ends inside a lane.
+// v - m - off (m rounded to binary32 and what that left), 0 stays at and past
+// cols: lanes that hold none of the row subtract 0, and elements are looked at
+// one by one only where a row ends inside a lane.
 template <int V>
-__device__ __forceinline__ void centre(float (&v)[V], float m, int32_t col, int32_t cols) {
+__device__ __forceinline__ void centre(float (&v)[V], float m, float off, int32_t col,
+                                       int32_t cols) {
   m = col < cols ? m : 0.0f;
+  off = col < cols ? off : 0.0f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) v[j] -= m;
+  for (int j = 0; j < V; ++j) v[j] = (v[j] - m) - off;
   if (cols % V != 0) {  // the same for every lane
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = col + j < cols ? v[j] : 0.0f;
@@ -113,7 +130,7 @@ __global__ __launch_bounds__((kThreads<W>), (kFwdWaves<T, NC>)) void k_norm_fwd(
     T* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd,
     uint8_t* __restrict__ q, uint8_t* __restrict__ e) {
   constexpr int V = kVec<T>, R = kRows<W>;
-  __shared__ float lds[2 * W];
+  __shared__ double lds[W];
   const int32_t groups = (cols + kAct8Group - 1) / kAct8Group;
   const int64_t stride = (int64_t)gridDim.x * R;
   int64_t r = (int64_t)blockIdx.x * R + (W == 1 ? threadIdx.x >> 6 : 0);
@@ -127,9 +144,9 @@ __global__ __launch_bounds__((kThreads<W>), (kFwdWaves<T, NC>)) void k_norm_fwd(
   load_params<T, NC, W>(gamma, cols, ga);
   load_params<T, NC, W>(beta, cols, be);
   const float n = (float)cols;
+  const double n64 = (double)cols, inv64 = 1.0 / n64;
   for (; r < rows; r += stride) {
     float v[NC][V];
-    float s = 0.0f, none = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) unpack_row<T>(next[c], chunk_col<T, W>(c), cols, v[c]);
     if (r + stride < rows) {
@@ -137,41 +154,36 @@ __global__ __launch_bounds__((kThreads<W>), (kFwdWaves<T, NC>)) void k_norm_fwd(
       for (int c = 0; c < NC; ++c)
         next[c] = load_raw(x + (r + stride) * ldx, chunk_col<T, W>(c), cols);
     }
+    // The sum is binary64: a binary32 one is off by the rounding of values of
+    // the mean's size, which xhat has in units of the spread (1e-3 of it at a
+    // mean of 1000 spreads), and a mean near 0 by that of the values.  Its
+    // quotient is put right by its remainder, so a constant row's is the value.
+    double s = 0.0;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int j = 0; j < V; ++j) s += v[c][j];
-    row_sum2<W>(s, none, lds);
-    const float mu = s / n;
-    float s1 = 0.0f, s2 = 0.0f;
+      for (int j = 0; j < V; ++j) s += (double)v[c][j];
+    s = row_sum<W>(s, lds);
+    const double m = s * inv64, mean64 = __builtin_fma(__builtin_fma(-m, n64, s), inv64, m);
+    const float mu = (float)mean64, off = (float)(mean64 - (double)mu);
+    float s2 = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
-      centre(v[c], mu, col, cols);
+      centre(v[c], mu, off, col, cols);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        s1 += v[c][j];
-        s2 += v[c][j] * v[c][j];
-      }
+      for (int j = 0; j < V; ++j) s2 += v[c][j] * v[c][j];
     }
-    row_sum2<W>(s1, s2, lds);
-    // what the centred values still sum to corrects the mean's rounding, which
-    // is of the mean's size and not of the spread's: in the mean (one near 0
-    // keeps its relative accuracy), in the variance and in the values
-    // themselves (a mean of 1000 spreads of binary32 rows left xhat 1e-3 off,
-    // constant rows not at 0)
-    const float off = s1 / n;
-    const float var = s2 / n - off * off;
-    const float rs = 1.0f / __builtin_sqrtf((var < 0.0f ? 0.0f : var) + eta);  // NaN stays
+    const float var = row_sum<W>(s2, reinterpret_cast<float*>(lds)) / n;
+    const float rs = 1.0f / __builtin_sqrtf(var + eta);
     if ((W == 1 ? threadIdx.x & 63 : threadIdx.x) == 0) {
-      mean[r] = mu + off;
+      mean[r] = mu;
       rstd[r] = rs;
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
       float o[V];
-      centre(v[c], off, col, cols);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         v[c][j] *= rs;

@@ -414,7 +414,7 @@ int oba_step_small(oba_layout layout, const void* g, int g_dtype, const float* m
  * those of no rows are 0.
  *
  * Arithmetic is binary32 (products of 16-bit operands exact, sums binary32 in
- * a fixed order), rounded once to each output: results are reproducible.  No
+ * a fixed order, a layer norm's mean from a binary64 sum), rounded once to each output: results are reproducible.  No
  * call allocates, and one workspace serves one call at a time.  rows = 0 is
  * allowed.  What a call writes, its workspace included, must not overlap any
  * other buffer of the call; what it only reads may.

@@ -82,3 +82,23 @@ def test_constant_rows(c, dtype):
     e1 = 50 * U * v.double()[:, 0]
     ev = 161 * U * e1 * e1  # as above, without a spread
     close(rstd, t.full_like(ev, ETA ** -0.5), ETA ** -0.5 * (0.6 * ev / ETA + 3 * U), "rstd")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("c", [7, 500, 1000, 1600, 4090, 8000, 16384])
+def test_mean_near_zero_keeps_its_relative_accuracy(c, dtype):
+    """Rows whose sum nearly cancels: each mean is its true value rounded once,
+    up to what binary64 loses of the sum (2^-53 of the magnitudes for each of
+    at most 16384 additions)."""
+    t = torch()
+    r = 40
+    say(f"[norm centre] {r}x{c} {dtype} means near 0")
+    g = gen(c + 1)
+    x = rows(g, r, c, dtype, std=1.0)
+    for k in range(3):  # takes the sum out of every row, up to the type's rounding
+        left = x.double().sum(1)
+        x[:, k] -= (left * (1 - 2.0 ** -9)).to(x.dtype)
+    y, mean, rstd, q, e = forward(x, t.ones(c, device="cuda"), t.zeros(c, device="cuda"))
+    m = x.double().sum(1) / c
+    lost = 2.0 ** -53 * 16384 * x.double().abs().mean(1)
+    close(mean, m, half("f32") * m.abs() * (1 + 2.0 ** -20) + lost, "mean")
