@@ -57,7 +57,7 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* lds) {
   }
 }
 
-// The same for one value, and for one in binary64 (`lds` holds W doubles).
+// The same for one value, and for one in binary64 (`lds` holds W values).
 template <int W, typename F>
 __device__ __forceinline__ F row_sum(F a, F* lds) {
   a = wave_sum(a);
@@ -130,7 +130,8 @@ __global__ __launch_bounds__((kThreads<W>), (kFwdWaves<T, NC>)) void k_norm_fwd(
     T* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd,
     uint8_t* __restrict__ q, uint8_t* __restrict__ e) {
   constexpr int V = kVec<T>, R = kRows<W>;
-  __shared__ double lds[W];
+  __shared__ double lds64[W];
+  __shared__ float lds[W];
   const int32_t groups = (cols + kAct8Group - 1) / kAct8Group;
   const int64_t stride = (int64_t)gridDim.x * R;
   int64_t r = (int64_t)blockIdx.x * R + (W == 1 ? threadIdx.x >> 6 : 0);
@@ -163,7 +164,7 @@ __global__ __launch_bounds__((kThreads<W>), (kFwdWaves<T, NC>)) void k_norm_fwd(
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) s += (double)v[c][j];
-    s = row_sum<W>(s, lds);
+    s = row_sum<W>(s, lds64);
     const double m = s * inv64, mean64 = __builtin_fma(__builtin_fma(-m, n64, s), inv64, m);
     const float mu = (float)mean64, off = (float)(mean64 - (double)mu);
     float s2 = 0.0f;
@@ -174,7 +175,7 @@ __global__ __launch_bounds__((kThreads<W>), (kFwdWaves<T, NC>)) void k_norm_fwd(
 #pragma unroll
       for (int j = 0; j < V; ++j) s2 += v[c][j] * v[c][j];
     }
-    const float var = row_sum<W>(s2, reinterpret_cast<float*>(lds)) / n;
+    const float var = row_sum<W>(s2, lds) / n;
     const float rs = 1.0f / __builtin_sqrtf(var + eta);
     if ((W == 1 ? threadIdx.x & 63 : threadIdx.x) == 0) {
       mean[r] = mu;

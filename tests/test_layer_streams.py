@@ -15,3 +15,25 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     assert c.stream(SimpleNamespace(device_index=0, cuda_stream=77)) == 77
     with pytest.raises(ValueError, match="stream"):
         c.stream(SimpleNamespace(device_index=1, cuda_stream=77))
+
+
+@pytest.mark.gpu
+def test_a_call_on_a_stream_of_its_own():
+    """An explicit stream is the one that the kernels run on: its work is
+    complete once it alone is waited for."""
+    import torch
+
+    side = torch.cuda.Stream()
+    x = torch.randn((3000, 1000), device="cuda").bfloat16()
+    q, e = oba.act8_buffers(*x.shape)
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    oba.act8_encode(x, q, e)
+    oba.act8_decode(q, e, y)
+    torch.cuda.synchronize()
+    q.zero_()
+    e.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    oba.act8_encode(x, q, e, stream=side)
+    oba.act8_decode(q, e, z, stream=side)
+    side.synchronize()
+    assert torch.equal(y, z)
