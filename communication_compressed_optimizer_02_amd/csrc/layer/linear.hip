@@ -22,17 +22,21 @@
 // One 128 x 128 tile serves all three: a step of 64 along k is 32 KB, loaded
 // straight to LDS (no registers, no LDS writes by the waves), so that three
 // blocks of four waves fit a CU and one's products hide the others' loads and
-// epilogues.  At 16384 x 1024 -> 4096 in bfloat16 (137 GFLOP; us): 148 bare,
-// 180 with GELU, 186-198 with GELU and the pre-activation kept, 145 the input
-// gradient, 200 with GELU's derivative from 8 bits, 171 the weight gradients
-// of 8 workers from 8 bits; the library's bare product takes 106.  A 256 x 256
-// tile of eight waves with two halves of LDS took 152 bare, but 208 with its
-// epilogue, which nothing hides; 128 x 256 took 140, 168 and 197, and 216 for
-// the input gradient with GELU's derivative.  What bounds it: at K = 1024 the
-// epilogue's vector instructions (about 36 a result with GELU kept) are as
-// long as the products; at K = 4096 the products run at 1.1 PFLOP/s, where LDS
-// is the nearest limit (64 KB of fragments and 32 KB of loads for 512 cycles
-// of products).
+// epilogues.  At 16384 x 1024 -> 4096 in bfloat16 (137 GFLOP; us in a steady
+// run, and a median of 12 calls under the profiler, whose clocks are lower):
+// 147 (158) bare, 167 with GELU, 189-196 (201-229) with GELU and the
+// pre-activation kept, 148 the input gradient, 190-204 (199-220) with GELU's
+// derivative from 8 bits, 171-176 (177-189) the weight gradients of 8 workers
+// from 8 bits; the library's bare product takes 108.  A 256 x 256 tile of eight
+// waves with two halves of LDS took 152 bare, but 208 with its epilogue, which
+// nothing hides; 128 x 256 took 140, 168 and 197, and 216 for the input gradient
+// with GELU's derivative.  What bounds it, by the counters: waiting.  The matrix
+// cores are busy for 42 % of a bare product at K = 1024 and 55 % at K = 4096
+// (1.13 PFLOP/s; the library 1.55), fragment reads keep LDS busy for 26 and 29 %,
+// and the waves wait for 46 and 50 % of their time: a step's loads are all waited
+// for before its products start, so only the other blocks of the CU cover them.
+// With GELU and the kept form a result takes 30 vector instructions instead of 8,
+// and the matrix cores are busy for 34 %.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -566,9 +570,10 @@ __global__ __launch_bounds__(WA* WB * 64, 3) void k_linear(Linear a, Tiles t) {
 // of the 8-bit form); its 8 waves share k in lines of 64, each wave's
 // fragments straight from memory (a line of w is used by one wave, once), all
 // of a batch's loads before its products.  The waves' sums meet in LDS, added
-// in wave order.  1 x 1600 -> 6400 (20 MB of w): 7.4 us, 2.8 TB/s, bound by the
-// loads' latency (two batches a wave) and 200 blocks for 256 CUs; split tiles
-// and their join took 9.0 + 5.0.
+// in wave order.  1 x 1600 -> 6400 (20 MB of w): 7.4 us, 2.8 TB/s.  All of this k
+// is one batch a wave (2048 to a batch of up to 32 rows), so each load's latency
+// is paid once; 200 blocks leave 56 of the 256 CUs idle, and of the 25 lines one
+// wave has four and the others three.  Split tiles and their join took 9.0 + 5.0.
 constexpr int kFewWaves = 8, kFewCols = 32;
 
 // The 8 elements of a row from k; those at or past K are 0.

@@ -1,21 +1,41 @@
 // norm.hip -- layer norm of rows, forward and backward (gfx950).
 //
-// Forward, per row: mean, rstd = 1/sqrt(var + eta) with the variance summed
-// from the centred values (two passes over registers, one over memory), then
+// Forward, per row: mean (a binary64 sum), rstd = 1/sqrt(var + eta) with the
+// variance summed from the centred values (two passes over registers, one over
+// memory), then
 // y = xhat * gamma + beta and, if wanted, xhat kept in 8 bits.  Backward, per
 // row, with a = dy * gamma:
 //   dx = rstd * (a - mean(a) - xhat * mean(a * xhat)) + add
 // and, per worker and column, dgamma = sum dy * xhat, dbeta = sum dy.
-// Everything is bound by the rows' bytes: a row is read once into registers.
+// A row is read once into registers.
 //
 // A row belongs to one wave up to 1024 columns, to a block of 4 waves up to
 // 4096 and of 8 waves up to 16384.  A wave walks many rows, so that gamma
 // and beta are read once and, in the backward pass, the column sums stay in
 // binary32 registers until the wave's last row; blocks write them as partial
 // sums, which a second kernel adds per column in binary64 in a fixed order.
-// 32768 x 1024 in bfloat16: forward with xhat kept 31 us (169 MB, 5.4 TB/s),
+// 32768 x 1024 in bfloat16: forward with xhat kept 32 us (169 MB, 5.3 TB/s),
 // backward from 8 bits with add 50 us (236 MB, 4.7 TB/s) and 4.8 us for the
 // columns' join; a large copy reaches 5.0 TB/s.
+//
+// What bounds it goes by the width.  2^25 elements in us, calls one after
+// another, forward bare, forward kept, backward from the rows and from 8 bits
+// (join included; the bytes at 4.96 TB/s take 27, 34, 41 and 34 in bfloat16, 54,
+// 61, 81 and 61 in binary32):
+//   columns      64   128   512  1024  2048  4096  8192 16384
+//   bfloat16    183    93    29    27    32    27    27    28
+//               214   113    37    34    38    35    34    39
+//               200   107    45    44    51    55    57    66
+//               237   129    48    43    58    56    61    74
+//   binary32    167    90    49    48    51    49    50    52
+//               201   107    57    58    59    58    59    63
+//               178   101    84    83    86    88    84   100
+//               176    98    65    69    69    75    88   115
+// Forward, the bytes bound every row from 512 columns on.  A narrower row still
+// takes a wave, whose sums and instructions bound it: at 64 columns 8 to 16 of
+// the 64 lanes hold data.  Backward, the bytes bound binary32 rows of 512 to
+// 4096 columns; other rows take 1.1 to 2.2 times the bytes' time, the more the
+// wider they are: above 1024 columns a block has one row in flight.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -117,7 +137,9 @@ template <int W>
 constexpr int kRows = W == 1 ? 4 : 1;
 
 // Waves per SIMD asked of the compiler: what the registers of a row of NC
-// pieces allow without spilling.
+// pieces allow without spilling.  One instance spills all the same, the
+// backward pass of binary32 rows above 8192 columns: 21 registers from the
+// rows (24 bytes a lane), 90 from 8 bits (108 bytes), at two waves.
 template <typename T, int NC>
 constexpr int kFwdWaves = NC * kVec<T> <= 16 ? 4 : 2;
 template <typename T, int NC>

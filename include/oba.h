@@ -414,10 +414,11 @@ int oba_step_small(oba_layout layout, const void* g, int g_dtype, const float* m
  * those of no rows are 0.
  *
  * Arithmetic is binary32 (products of 16-bit operands exact, sums binary32 in
- * a fixed order, a layer norm's mean from a binary64 sum), rounded once to each output: results are reproducible.  No
- * call allocates, and one workspace serves one call at a time.  rows = 0 is
- * allowed.  What a call writes, its workspace included, must not overlap any
- * other buffer of the call; what it only reads may.
+ * a fixed order, a layer norm's mean from a binary64 sum), rounded once to each
+ * output: results are reproducible.  No call allocates, and one workspace
+ * serves one call at a time.  rows = 0 is allowed.  What a call writes, its
+ * workspace included, must not overlap any other buffer of the call; what it
+ * only reads may.
  *
  * 8-bit form of a [rows][cols] matrix: G = ceil(cols / 32) groups of 32
  * columns; q: [rows][32*G] integers (16-byte aligned, those past cols 0), e:
