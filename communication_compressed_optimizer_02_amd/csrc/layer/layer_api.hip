@@ -5,7 +5,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "abi.hpp"
+#include "checks.hpp"
 #include "layer_kernels.hpp"
 #include "oba.h"
 
@@ -14,41 +14,6 @@ static_assert(OBA_ACT8_GROUP == oba::kAct8Group, "group size");
 namespace {
 
 using oba::LinearKind;
-
-template <class F>
-int launch(const char* name, hipStream_t st, F&& fn) {
-  return oba::abi_launch(name, st, [](void* f) { (*static_cast<F*>(f))(); }, &fn);
-}
-
-bool is_type(int t) { return t == OBA_F32 || t == OBA_F16 || t == OBA_BF16; }
-int size_of(int t) { return t == OBA_F32 ? 4 : 2; }
-
-int check_ptr(const void* p, uintptr_t align) {
-  if (!p) return OBA_EINVAL;
-  return ((uintptr_t)p & (align - 1)) ? OBA_EALIGN : OBA_OK;
-}
-
-bool sizes_ok(int64_t rows, int64_t cols, int64_t most_cols) {
-  return rows >= 0 && rows <= oba::kMaxRows && cols >= 1 && cols <= most_cols;
-}
-bool ld_ok(int64_t ld, int64_t cols) {
-  return ld >= cols && ld % 8 == 0 && ld <= oba::kMaxLd;
-}
-// n workers of `rows` rows
-bool workers_ok(int32_t n, int64_t rows) {
-  return n >= 1 && n <= 4096 && rows >= 0 && rows <= oba::kMaxRows / n;
-}
-int check_kept(const int8_t* q, const uint8_t* e) {
-  if (!q || !e) return OBA_EINVAL;
-  return check_ptr(q, 16);
-}
-bool act_ok(int act) { return act >= OBA_ACT_NONE && act <= OBA_ACT_GELU_TANH; }
-
-#define OBA_TRY(expr)              \
-  do {                             \
-    int rc_ = (expr);              \
-    if (rc_ != OBA_OK) return rc_; \
-  } while (0)
 
 size_t norm_ws(int32_t n, int64_t rows, int64_t cols) {
   return (size_t)n * oba::norm_bwd_blocks(n, rows, (int32_t)cols) * 2 * cols * sizeof(float);
@@ -66,12 +31,6 @@ int run_linear(const char* name, LinearKind kind, const oba::Linear& a, hipStrea
     if (oba::linear_splits(kind, a.n, a.rows, a.cols, a.k) > 1)
       oba::launch_linear_join(kind, a, stream);
   });
-}
-
-int check_ws(const void* ws, size_t have, size_t need) {
-  if (need == 0) return OBA_OK;
-  OBA_TRY(check_ptr(ws, 16));
-  return have < need ? OBA_EWORKSPACE : OBA_OK;
 }
 
 }  // namespace

@@ -43,18 +43,11 @@
 
 #include "layer.hpp"
 #include "layer_kernels.hpp"
+#include "rows.hpp"
 
 namespace oba {
 
 namespace {
-
-// A lane's columns: chunk c holds kVec consecutive columns from
-// (c * W * 64 + thread) * kVec, W the waves that share a row.
-template <typename T, int W>
-__device__ __forceinline__ int32_t chunk_col(int c) {
-  const int32_t t = W == 1 ? (int32_t)(threadIdx.x & 63) : (int32_t)threadIdx.x;
-  return (c * W * 64 + t) * kVec<T>;
-}
 
 // Sums of two values over the waves of a row; every lane gets them.  `lds`
 // holds 2 * W floats; the sums of the waves are added in wave order.
@@ -89,45 +82,6 @@ __device__ __forceinline__ F row_sum(F a, F* lds) {
     for (int w = 0; w < W; ++w) a += lds[w];
   }
   return a;
-}
-
-// Columns from a binary32 vector of any alignment (parameters live anywhere
-// in the flat x); those past cols read as 0.
-struct __attribute__((packed, aligned(4))) Four {
-  float v[4];
-};
-template <typename T, int NC, int W>
-__device__ __forceinline__ void load_params(const float* __restrict__ p, int32_t cols,
-                                            float (&v)[NC][kVec<T>]) {
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int32_t col = chunk_col<T, W>(c);
-#pragma unroll
-    for (int j = 0; j < kVec<T>; j += 4) {
-      if (col + j + 4 <= cols) {
-        const Four f = *reinterpret_cast<const Four*>(p + col + j);
-        for (int i = 0; i < 4; ++i) v[c][j + i] = f.v[i];
-      } else {
-        for (int i = 0; i < 4; ++i) v[c][j + i] = col + j + i < cols ? p[col + j + i] : 0.0f;
-      }
-    }
-  }
-}
-
-// v - m - off (m rounded to binary32 and what that left), 0 stays at and past
-// cols: lanes that hold none of the row subtract 0, and elements are looked at
-// one by one only where a row ends inside a lane.
-template <int V>
-__device__ __forceinline__ void centre(float (&v)[V], float m, float off, int32_t col,
-                                       int32_t cols) {
-  m = col < cols ? m : 0.0f;
-  off = col < cols ? off : 0.0f;
-#pragma unroll
-  for (int j = 0; j < V; ++j) v[j] = (v[j] - m) - off;
-  if (cols % V != 0) {  // the same for every lane
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = col + j < cols ? v[j] : 0.0f;
-  }
 }
 
 // The waves of a block: 4 rows at a time with a wave each, or one row.
