@@ -12,6 +12,9 @@ from .binding import (OBA_BF16, OBA_F16, OBA_F32, Layout, ObaError, Plateau, Sta
                       act8_buffers, act8_decode, act8_encode, layer_norm, layer_norm_backward,
                       layer_norm_backward_workspace, linear, linear_input_grad,
                       linear_weight_grad, linear_weight_grad_workspace, linear_workspace,
+                      dropout, dropout_rng, gated_hidden_grad, gated_hidden_grad_workspace,
+                      gated_linear, gated_linear_workspace, residual_norm,
+                      residual_norm_backward, residual_norm_backward_workspace,
                       server_momentum, server_reduce_recompress,
                       server_reduce_recompress_deferred, step_small, timing_enable, timing_read, timing_reset, validate)
 from .feedforward import FeedForward
@@ -29,4 +32,7 @@ __all__ = [
     "act8_buffers", "act8_decode", "act8_encode", "layer_norm", "layer_norm_backward",
     "layer_norm_backward_workspace", "linear", "linear_input_grad", "linear_weight_grad",
     "linear_weight_grad_workspace", "linear_workspace",
+    "dropout", "dropout_rng", "gated_hidden_grad", "gated_hidden_grad_workspace", "gated_linear",
+    "gated_linear_workspace", "residual_norm", "residual_norm_backward",
+    "residual_norm_backward_workspace",
 ]

@@ -12,7 +12,7 @@ Buffers (all CUDA tensors on the layout's device, C-contiguous):
   wbits  [n][W]  int64 (packed 64-bit words)   sbits [W] int64
   wscale [n][n_wseg] float32                   sscale [n_sseg] float32
 
-The layer calls (act8_*, layer_norm*, linear*) take matrices as 2-D tensors
+The layer calls (act8_*, layer_norm*, linear*, gated_*, residual_norm*, dropout) take matrices as 2-D tensors
 with rows of a stride that is a multiple of 8 elements (columns adjacent),
 and activations kept in 8 bits as the pair (q, e) of act8_buffers().  Their
 tensors and the stream must be on the current device, and what a call writes
@@ -32,6 +32,7 @@ _lib = None
 # name -> (restype, argtypes); mirrors include/oba.h
 _P, _I64, _I32, _D, _SZ, _I = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_double,
                                ctypes.c_size_t, ctypes.c_int)
+_U32 = ctypes.c_uint32
 SIGNATURES = {
     "oba_version": (_I, []),
     "oba_status_string": (ctypes.c_char_p, [_I]),
@@ -79,6 +80,19 @@ SIGNATURES = {
     "oba_linear_weight_grad_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64]),
     "oba_linear_weight_grad": (_I, [_I32, _I64, _I64, _I64, _P, _I64, _I, _P, _P, _P, _P, _I, _I64,
                                     _P, _SZ, _P]),
+    "oba_dropout": (_I, [_I64, _I64, _P, _I64, _I, _D, _P, _U32, _P, _I64, _P, _I64, _P]),
+    "oba_residual_norm": (_I, [_I64, _I64, _I, _I, _D, _P, _I64, _D, _P, _I64, _P, _P, _P, _D, _P,
+                               _U32, _P, _P, _P, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, _P]),
+    "oba_residual_norm_backward_workspace_bytes": (_SZ, [_I32, _I64, _I64]),
+    "oba_residual_norm_backward": (_I, [_I32, _I64, _I64, _I, _I, _P, _I64, _P, _P, _P, _P, _P,
+                                        _I64, _D, _P, _I64, _P, _P, _P, _P, _P, _P, _D, _P, _U32,
+                                        _P, _I64, _P, _P, _P, _P, _P, _I, _I64, _P, _SZ, _P]),
+    "oba_gated_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "oba_gated_linear": (_I, [_I64, _I64, _I64, _P, _I64, _P, _I64, _I, _P, _I, _P, _I64, _P, _P,
+                              _P, _P, _P, _P, _P, _SZ, _P]),
+    "oba_gated_hidden_grad_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "oba_gated_hidden_grad": (_I, [_I64, _I64, _I64, _P, _I64, _P, _I64, _I, _I, _P, _P, _P, _P,
+                                   _P, _I64, _P, _SZ, _P]),
     "oba_timing_enable": (_I, [_I, _I32]),
     "oba_timing_read": (_I, [ctypes.c_char_p, ctypes.POINTER(_D), ctypes.POINTER(_I64)]),
     "oba_timing_reset": (_I, []),
@@ -568,6 +582,8 @@ def step_small(L: Layout, g, m, c, wbits, wscale, a, sbits, sscale, denom, m_out
 
 ACT8_GROUP = 32
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3}
+NORMS = {"layer": 0, "rms": 1}
+GATES = {**ACTS, "silu": 4, "sigmoid": 5}
 _TYPES = {}     # torch dtype -> OBA code
 _torch_module = None
 
@@ -681,6 +697,21 @@ class _Call:
             taken.append((at, at + length))
             out.append(base + at * size)
         return _TYPES[g.dtype], ld, out
+
+    def opt(self, t, name, size):
+        """Pointer of a float32 vector, or of none."""
+        return None if t is None else self.vec(t, name, size)
+
+    def rng(self, t):
+        """Pointer of a dropout's {seed, step}, or of none."""
+        if t is None:
+            return None
+        self._on(t, "rng")
+        if t.dtype != self.torch.int64:
+            raise TypeError(f"rng: dtype {t.dtype} != torch.int64")
+        if t.numel() != 2 or not t.is_contiguous():
+            raise ValueError(f"rng: expected 2 contiguous elements, got {tuple(t.shape)}")
+        return t.data_ptr()
 
     def ws(self, ws):
         if ws is None:
@@ -828,6 +859,138 @@ def linear_weight_grad(n, dy, q, e, g, n_in, at_w, at_bias, ws, stream=None):
     _check(lib().oba_linear_weight_grad(
         n, total // n, n_in, n_out, dyp, lddy, _TYPES[dy.dtype], qp, ep, gp, bp, gt, ldg, sp,
         sb, c.stream(stream)), "oba_linear_weight_grad")
+
+
+def dropout_rng(seed, step=0):
+    """The device's {seed, step} that dropout and residual_norm read: int64 [2].
+    A training step ends with rng[1] += 1, also inside a captured one."""
+    import torch
+
+    return torch.tensor([seed, step], dtype=torch.int64, device="cuda")
+
+
+def dropout(x, y, rng, rate, site=0, add=None, stream=None):
+    """y = x / (1 - rate) where kept, else 0, plus add; on dy the backward pass.
+    The mask is a function of rng, site and the place alone.  rng: of
+    dropout_rng() (None where nothing is dropped)."""
+    c = _Call()
+    xp, ldx = c.rows(x, "x")
+    rows, cols = x.shape
+    yp, ldy = c.rows(y, "y", rows, cols, x.dtype)
+    ap, lda = c.rows(add, "add", rows, cols, x.dtype) if add is not None else (None, 0)
+    _check(lib().oba_dropout(rows, cols, xp, ldx, _TYPES[x.dtype], rate, c.rng(rng), site, ap, lda,
+                             yp, ldy, c.stream(stream)), "oba_dropout")
+
+
+def residual_norm(x, eta, b=None, alpha=1.0, gate=None, gamma_b=None, beta_b=None, rstd_b=None,
+                  qb=None, eb=None, rate=0.0, rng=None, site=0, r=None, gamma=None, beta=None,
+                  z=None, rstd=None, q=None, e=None, kind="layer", stream=None):
+    """r = alpha x + gate * dropout(norm(b) * gamma_b + beta_b) and
+    z = norm(r) * gamma + beta, kind "layer" or "rms".  Without gamma_b no norm of
+    b, without gamma none of r; r or z may be left out.  With (qb, eb) norm(b)
+    (or b) is kept in 8 bits, with (q, e) norm(r); rstd_b and rstd [rows] float32
+    are written."""
+    c = _Call()
+    xp, ldx = c.rows(x, "x")
+    rows, cols = x.shape
+    dt = x.dtype
+    bp, ldb = c.rows(b, "b", rows, cols, dt) if b is not None else (None, 0)
+    rp, ldr = c.rows(r, "r", rows, cols, dt) if r is not None else (None, 0)
+    zp, ldz = c.rows(z, "z", rows, cols, dt) if z is not None else (None, 0)
+    qbp, ebp = c.kept(qb, eb, rows, cols)
+    qp, ep = c.kept(q, e, rows, cols)
+    _check(lib().oba_residual_norm(
+        rows, cols, _TYPES[dt], NORMS[kind], eta, xp, ldx, alpha, bp, ldb,
+        c.opt(gamma_b, "gamma_b", cols), c.opt(beta_b, "beta_b", cols), c.opt(gate, "gate", cols),
+        rate, c.rng(rng), site, c.opt(rstd_b, "rstd_b", rows), qbp, ebp, rp, ldr,
+        c.opt(gamma, "gamma", cols), c.opt(beta, "beta", cols), zp, ldz,
+        c.opt(rstd, "rstd", rows), qp, ep, c.stream(stream)), "oba_residual_norm")
+
+
+def residual_norm_backward_workspace(n, rows, cols):
+    """A workspace for residual_norm_backward of n workers with `rows` rows each."""
+    return _workspace(lib().oba_residual_norm_backward_workspace_bytes(n, rows, cols))
+
+
+def residual_norm_backward(n, dx, g, ws, dz=None, dr=None, alpha=1.0, q=None, e=None, rstd=None,
+                           gamma=None, at_gamma=None, at_beta=None, db=None, qb=None, eb=None,
+                           rstd_b=None, gamma_b=None, beta_b=None, gate=None, at_gate=None,
+                           at_gamma_b=None, at_beta_b=None, rate=0.0, rng=None, site=0,
+                           kind="layer", stream=None):
+    """dx and db from dz (the gradient of z, with q, e, rstd and gamma) and dr (the
+    gradient that r gets elsewhere), and every worker's gradients of the
+    parameters at these offsets of its row of g [n][ld] (None: not wanted)."""
+    c = _Call()
+    dxp, lddx = c.rows(dx, "dx")
+    total, cols = dx.shape
+    dt = dx.dtype
+    if n < 1 or total % n:
+        raise ValueError(f"dx: {total} rows are not {n} equal parts")
+    dzp, lddz = c.rows(dz, "dz", total, cols, dt) if dz is not None else (None, 0)
+    drp, lddr = c.rows(dr, "dr", total, cols, dt) if dr is not None else (None, 0)
+    dbp, lddb = c.rows(db, "db", total, cols, dt) if db is not None else (None, 0)
+    qp, ep = c.kept(q, e, total, cols)
+    qbp, ebp = c.kept(qb, eb, total, cols)
+    places = (at_gamma, at_beta, at_gamma_b, at_beta_b, at_gate)
+    if all(at is None for at in places):
+        gt, ldg, gp = OBA_F32, 0, (None,) * 5
+    else:
+        gt, ldg, gp = c.grads(g, n, *((at, cols) for at in places))
+    wp, wb = c.ws(ws)
+    _check(lib().oba_residual_norm_backward(
+        n, total // n, cols, _TYPES[dt], NORMS[kind], dzp, lddz, qp, ep,
+        c.opt(rstd, "rstd", total), c.opt(gamma, "gamma", cols), drp, lddr, alpha, dxp, lddx,
+        qbp, ebp, c.opt(rstd_b, "rstd_b", total), c.opt(gamma_b, "gamma_b", cols),
+        c.opt(beta_b, "beta_b", cols), c.opt(gate, "gate", cols), rate, c.rng(rng), site,
+        dbp, lddb, *gp, gt, ldg, wp, wb, c.stream(stream)), "oba_residual_norm_backward")
+
+
+def gated_linear_workspace(rows, n_in, hidden):
+    """A workspace for gated_linear of these sizes."""
+    return _workspace(lib().oba_gated_linear_workspace_bytes(rows, n_in, hidden))
+
+
+def gated_linear(x, w, y, ws, bias=None, gate="silu", qp=None, ep=None, qu=None, eu=None, q=None,
+                 e=None, stream=None):
+    """y = f(x wg^T + bg) * (x wu^T + bu) (float16 or bfloat16): w [2*hidden][in]
+    and bias [2*hidden] float32 hold the gate's part first.  With (qp, ep) and
+    (qu, eu) both pre-activations are kept in 8 bits, with (q, e) y is."""
+    c = _Call()
+    xp, ldx = c.rows(x, "x")
+    rows, n_in = x.shape
+    yp, ldy = c.rows(y, "y", rows, None, x.dtype)
+    hidden = y.shape[1]
+    wp, ldw = c.rows(w, "w", 2 * hidden, n_in, x.dtype)
+    kept = (*c.kept(qp, ep, rows, hidden), *c.kept(qu, eu, rows, hidden),
+            *c.kept(q, e, rows, hidden))
+    sp, sb = c.ws(ws)
+    _check(lib().oba_gated_linear(
+        rows, n_in, hidden, xp, ldx, wp, ldw, _TYPES[x.dtype], c.opt(bias, "bias", 2 * hidden),
+        GATES[gate], yp, ldy, *kept, sp, sb, c.stream(stream)), "oba_gated_linear")
+
+
+def gated_hidden_grad_workspace(rows, hidden, n_out):
+    """A workspace for gated_hidden_grad of these sizes."""
+    return _workspace(lib().oba_gated_hidden_grad_workspace_bytes(rows, hidden, n_out))
+
+
+def gated_hidden_grad(dy, w, qp, ep, qu, eu, dpu, ws, gate="silu", stream=None):
+    """dpu [rows][2*hidden] = [d * u * f'(p), d * f(p)] with d = dy w, w
+    [n_out][hidden] of the product behind the gate, p and u as kept.
+    linear_input_grad and linear_weight_grad with 2*hidden outputs go on from it."""
+    c = _Call()
+    dyp, lddy = c.rows(dy, "dy")
+    rows, n_out = dy.shape
+    wp, ldw = c.rows(w, "w", n_out, None, dy.dtype)
+    hidden = w.shape[1]
+    dp, ldd = c.rows(dpu, "dpu", rows, 2 * hidden, dy.dtype)
+    if qp is None or qu is None:
+        raise ValueError("qp, ep, qu, eu: both pre-activations kept in 8 bits are needed")
+    kept = (*c.kept(qp, ep, rows, hidden), *c.kept(qu, eu, rows, hidden))
+    sp, sb = c.ws(ws)
+    _check(lib().oba_gated_hidden_grad(
+        rows, hidden, n_out, dyp, lddy, wp, ldw, _TYPES[dy.dtype], GATES[gate], *kept, dp, ldd, sp,
+        sb, c.stream(stream)), "oba_gated_hidden_grad")
 
 
 def timing_enable(on=True, capacity=4096):

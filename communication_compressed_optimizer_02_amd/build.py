@@ -36,8 +36,8 @@ HIP_FLAGS = [
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra"]
 # one translation unit per pass, plus the C ABI
 HIP_SOURCES = ("warmup.hip", "compress.hip", "scales.hip", "server.hip", "update.hip",
-               "small.hip", "layer/act8.hip", "layer/norm.hip", "layer/linear.hip",
-               "layer/layer_api.hip", "api.hip")
+               "small.hip", "layer/act8.hip", "layer/norm.hip", "layer/linear.hip", "layer/dropout.hip", "layer/join.hip", "layer/gated.hip",
+               "layer/layer_api.hip", "layer/sublayer_api.hip", "api.hip")
 
 
 def hipcc() -> str:

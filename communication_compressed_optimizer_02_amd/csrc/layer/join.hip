@@ -1,0 +1,589 @@
+// join.hip -- what lies between two blocks of a residual network, in one pass
+// (gfx950): the norm behind a block, dropout, its gate, the residual sum and the
+// norm before the next block.
+//
+// Forward, per row, every step optional but the sum:
+//   n = norm(b) * gamma_b + beta_b,   r = alpha * x + gate * drop(n),
+//   z = norm(r) * gamma + beta
+// norm(v) = (v - mean) * rstd with rstd = 1 / sqrt(mean((v - mean)^2) + eta), or
+// without the mean (kind kNormRms).  Backward, with h = norm(r) and k = norm(b)
+// from 8 bits, per row and with a = dz * gamma:
+//   D = rstd * (a - mean(a) - h * mean(a * h)) + dr,   dx = alpha * D
+//   e = drop(D),   c = e * gate * gamma_b
+//   db = rstd_b * (c - mean(c) - k * mean(c * k))
+// (without mean(a) and mean(c) for kNormRms) and per worker and column four
+// sums, from which all parameters' gradients come:
+//   dgamma = sum dz * h, dbeta = sum dz, S = sum e * k, T = sum e:
+//   dgamma_b = gate * S, dbeta_b = gate * T, dgate = gamma_b * S + beta_b * T
+//
+// A row is read once into registers: eight columns a lane, by 1 to 16 waves (16
+// columns a lane above 8192).  A block walks many rows, so parameters are read
+// once and the column sums stay in binary32 registers until its last row; they
+// are written as partial sums and added per column in binary64 in a fixed
+// order.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "layer.hpp"
+#include "philox.hpp"
+#include "rows.hpp"
+#include "sublayer_kernels.hpp"
+
+namespace oba {
+
+namespace {
+
+// W waves to a row; blocks of 8 waves hold 8 / W rows at a time, 16 waves one.
+template <int W>
+constexpr int kThreads = W == 16 ? 1024 : 512;
+template <int W>
+constexpr int kRows = kThreads<W> / 64 / W;
+
+// Sums of two values over a row's W waves: every lane gets them, added in wave
+// order.  One barrier: two calls in turn use the two halves of `lds`, and a wave
+// that writes a half again has passed the barrier of the call between, behind
+// every wave's reads of this half.  All waves of a block call it together.
+template <int W, typename F>
+__device__ __forceinline__ void row_sums(F& a, F& b, F (*lds)[2][kThreads<W> / 64], int& half) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (W > 1) {
+    const int w = threadIdx.x >> 6, first = w & ~(W - 1);
+    if ((threadIdx.x & 63) == 0) {
+      lds[half][0][w] = a;
+      lds[half][1][w] = b;
+    }
+    __syncthreads();
+    a = b = 0;
+    for (int i = 0; i < W; ++i) {
+      a += lds[half][0][first + i];
+      b += lds[half][1][first + i];
+    }
+    half ^= 1;
+  }
+}
+
+// Columns of a row that its wave w holds.
+template <typename T, int NC, int W>
+__device__ __forceinline__ int32_t wave_cols(int32_t w, int32_t cols) {
+  int32_t n = 0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) n += min(max(cols - (c * W + w) * 64 * kVec<T>, 0), 64 * kVec<T>);
+  return n;
+}
+
+// Rows to their normalised form in place; the reciprocal of the spread.  The
+// mean comes from binary64 sums (a binary32 one is off by the rounding of values
+// of the mean's size), the squares from values centred on their wave's mean; the
+// waves' squares are moved to the row's mean, n_w (mean_w - mean)^2 each, so one
+// exchange serves both.  Quotients are put right by their remainders: a constant
+// row's mean is its value.
+template <typename T, int NC, int W>
+__device__ __forceinline__ float normalise(float (&v)[NC][kVec<T>], int32_t cols, int kind,
+                                           float eta, double (*lds)[2][kThreads<W> / 64],
+                                           int& half) {
+  constexpr int V = kVec<T>;
+  double mean = 0.0, squares;
+  if (kind == kNormLayer) {
+    double s = 0.0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) s += (double)v[c][j];
+    s = wave_sum(s);
+    auto quotient = [](double s, double n) {
+      const double inv = n > 0.0 ? 1.0 / n : 0.0, m = s * inv;
+      return __builtin_fma(__builtin_fma(-m, n, s), inv, m);
+    };
+    const int w = W == 1 ? 0 : (int)(threadIdx.x >> 6) & (W - 1);
+    mean = quotient(s, (double)wave_cols<T, NC, W>(w, cols));
+    const float mu = (float)mean, off = (float)(mean - (double)mu);
+    float s2 = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float t[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) t[j] = v[c][j];
+      centre(t, mu, off, chunk_col<T, W>(c), cols);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s2 = __builtin_fmaf(t[j], t[j], s2);
+    }
+    squares = (double)wave_sum(s2);
+    if constexpr (W > 1) {
+      const int wave = threadIdx.x >> 6, first = wave & ~(W - 1);
+      if ((threadIdx.x & 63) == 0) {
+        lds[half][0][wave] = s;
+        lds[half][1][wave] = squares;
+      }
+      __syncthreads();
+      s = 0.0;
+      for (int i = 0; i < W; ++i) s += lds[half][0][first + i];
+      mean = quotient(s, (double)cols);
+      squares = 0.0;
+      for (int i = 0; i < W; ++i) {
+        const double n = (double)wave_cols<T, NC, W>(i, cols);
+        const double d = quotient(lds[half][0][first + i], n) - mean;
+        squares += n > 0.0 ? __builtin_fma(n * d, d, lds[half][1][first + i]) : 0.0;
+      }
+      half ^= 1;
+    }
+  } else {
+    float s2 = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) s2 = __builtin_fmaf(v[c][j], v[c][j], s2);
+    s2 = wave_sum(s2);
+    squares = (double)s2;
+    if constexpr (W > 1) {
+      const int wave = threadIdx.x >> 6, first = wave & ~(W - 1);
+      if ((threadIdx.x & 63) == 0) lds[half][0][wave] = squares;
+      __syncthreads();
+      squares = 0.0;
+      for (int i = 0; i < W; ++i) squares += lds[half][0][first + i];
+      half ^= 1;
+    }
+  }
+  const float rs = 1.0f / __builtin_sqrtf((float)(squares / (double)cols) + eta);
+  const float mu = (float)mean, off = (float)(mean - (double)mu);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if (kind == kNormLayer) centre(v[c], mu, off, chunk_col<T, W>(c), cols);
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[c][j] *= rs;
+  }
+  return rs;
+}
+
+// A lane's columns of a row to 8 bits; four or eight lanes hold a group.
+template <typename T>
+__device__ __forceinline__ void keep(const float (&v)[kVec<T>], int8_t* q, uint8_t* e, int64_t row,
+                                     int32_t groups, int32_t col) {
+  constexpr int V = kVec<T>;
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) top = max(top, magnitude(v[j]));
+  top = max_lanes<kAct8Group / V>(top);
+  const uint32_t ex = group_exp(top);
+  const float inv = inv_step_of(ex), step = step_of(ex);
+  if (col >= groups * kAct8Group) return;  // a started group is written whole
+  int8_t* at = q + row * (int64_t)groups * kAct8Group + col;
+  if constexpr (V == 8)
+    *reinterpret_cast<lu2*>(at) =
+        lu2{quant4(v, inv, step, ex != 255u), quant4(v + 4, inv, step, ex != 255u)};
+  else
+    *reinterpret_cast<uint32_t*>(at) = quant4(v, inv, step, ex != 255u);
+  if (col % kAct8Group == 0) e[row * groups + col / kAct8Group] = (uint8_t)ex;
+}
+
+template <typename T, int NC, int W>
+__device__ __forceinline__ void params_or(const float* p, int32_t cols, float other,
+                                          float (&v)[NC][kVec<T>]) {
+  if (p) {
+    load_params<T, NC, W>(p, cols, v);
+  } else {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < kVec<T>; ++j) v[c][j] = other;
+  }
+}
+
+// Waves per SIMD asked of the compiler.
+template <typename T, int NC>
+constexpr int kWaves = NC * kVec<T> <= 8 ? 4 : 2;
+
+template <typename T, int NC, int W>
+__global__ __launch_bounds__((kThreads<W>), (kWaves<T, NC>)) void k_join_fwd(JoinFwd a) {
+  constexpr int V = kVec<T>, R = kRows<W>;
+  __shared__ double lds[2][2][kThreads<W> / 64];
+  int half = 0;
+  const int32_t cols = a.cols, groups = (cols + kAct8Group - 1) / kAct8Group;
+  const int64_t stride = (int64_t)gridDim.x * R;
+  const bool first_lane = (threadIdx.x & (W * 64 - 1)) == 0;
+  const RngKey key = load_key(a.drop);
+  int64_t r = (int64_t)blockIdx.x * R + threadIdx.x / (W * 64);
+  // a row ahead: its loads are in flight while this one is worked on
+  lu4 nx[NC], nb[NC];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int32_t col = chunk_col<T, W>(c);
+      nx[c] = load_raw(static_cast<const T*>(a.x) + row * a.ldx, col, cols);
+      if (a.b) nb[c] = load_raw(static_cast<const T*>(a.b) + row * a.ldb, col, cols);
+    }
+  };
+  if (r < a.rows) load(r);
+  float gate[NC][V], gb[NC][V], bb[NC][V], ga[NC][V], be[NC][V];
+  params_or<T, NC, W>(a.gate, cols, 1.0f, gate);
+  params_or<T, NC, W>(a.gamma_b, cols, 1.0f, gb);
+  params_or<T, NC, W>(a.beta_b, cols, 0.0f, bb);
+  params_or<T, NC, W>(a.gamma, cols, 1.0f, ga);
+  params_or<T, NC, W>(a.beta, cols, 0.0f, be);
+  // the rows of a block go round together: its waves meet at the sums' barriers
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += stride, r += stride) {
+    const bool in = r < a.rows;
+    float x[NC][V], v[NC][V];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int32_t col = chunk_col<T, W>(c);
+      unpack_row<T>(in ? nx[c] : lu4{0u, 0u, 0u, 0u}, col, cols, x[c]);
+      unpack_row<T>(in && a.b ? nb[c] : lu4{0u, 0u, 0u, 0u}, col, cols, v[c]);
+    }
+    if (r + stride < a.rows) load(r + stride);
+    if (a.b) {
+      if (a.gamma_b) {
+        const float rs = normalise<T, NC, W>(v, cols, a.kind, a.eta, lds, half);
+        if (in && first_lane) a.rstd_b[r] = rs;
+      }
+      if (a.qb && in) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) keep<T>(v[c], a.qb, a.eb, r, groups, chunk_col<T, W>(c));
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (a.gamma_b) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(v[c][j], gb[c][j], bb[c][j]);
+        }
+        if (a.drop.threshold) drop<V>(a.drop, key, r, (cols + 7) / 8, chunk_col<T, W>(c), v[c]);
+        if (a.gate) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[c][j] *= gate[c][j];
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int32_t col = chunk_col<T, W>(c);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[c][j] = __builtin_fmaf(a.alpha, x[c][j], v[c][j]);
+      if (a.r && in && col < cols) store_row(static_cast<T*>(a.r) + r * a.ldr, col, cols, x[c]);
+    }
+    if (!a.gamma) continue;
+    const float rs = normalise<T, NC, W>(x, cols, a.kind, a.eta, lds, half);
+    if (!in) continue;
+    if (first_lane) a.rstd[r] = rs;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int32_t col = chunk_col<T, W>(c);
+      if (a.q) keep<T>(x[c], a.q, a.e, r, groups, col);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[c][j] = __builtin_fmaf(x[c][j], ga[c][j], be[c][j]);
+      if (col < cols) store_row(static_cast<T*>(a.z) + r * a.ldz, col, cols, x[c]);
+    }
+  }
+}
+
+// ---- backward ------------------------------------------------------------------
+// What a row's backward pass reads, as it lies in memory.
+template <int NC>
+struct BwdRow {
+  lu4 dz[NC], dr[NC];
+  lu2 q[NC], qb[NC];
+  uint32_t e[NC], eb[NC];
+  float rs, rsb;
+};
+
+template <typename T>
+__device__ __forceinline__ void load_kept(const int8_t* q, const uint8_t* e, int64_t row,
+                                          int32_t groups, int32_t col, int32_t cols, lu2& qr,
+                                          uint32_t& er) {
+  qr = lu2{0u, 0u};
+  er = 0u;
+  if (col < cols) {
+    const int8_t* at = q + row * (int64_t)groups * kAct8Group + col;
+    if constexpr (kVec<T> == 8) qr = *reinterpret_cast<const lu2*>(at);
+    else qr[0] = *reinterpret_cast<const uint32_t*>(at);
+    er = e[row * groups + col / kAct8Group];
+  }
+}
+
+template <typename T, int NC, int W>
+__device__ __forceinline__ void load_bwd(const JoinBwd& a, int64_t r, int32_t groups,
+                                         BwdRow<NC>& w) {
+  if (a.dz) w.rs = a.rstd[r];
+  if (a.gamma_b) w.rsb = a.rstd_b[r];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int32_t col = chunk_col<T, W>(c);
+    if (a.dz) {
+      w.dz[c] = load_raw(static_cast<const T*>(a.dz) + r * a.lddz, col, a.cols);
+      load_kept<T>(a.q, a.e, r, groups, col, a.cols, w.q[c], w.e[c]);
+    }
+    if (a.dr) w.dr[c] = load_raw(static_cast<const T*>(a.dr) + r * a.lddr, col, a.cols);
+    if (a.qb) load_kept<T>(a.qb, a.eb, r, groups, col, a.cols, w.qb[c], w.eb[c]);
+  }
+}
+
+// The norm's input gradient from that of its normalised rows, in place.
+template <typename T, int NC, int W>
+__device__ __forceinline__ void through(float (&d)[NC][kVec<T>], const float (&h)[NC][kVec<T>],
+                                        float rs, int32_t cols, int kind,
+                                        float (*lds)[2][kThreads<W> / 64], int& half) {
+  constexpr int V = kVec<T>;
+  float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      s1 += d[c][j];
+      s2 = __builtin_fmaf(d[c][j], h[c][j], s2);
+    }
+  row_sums<W>(s1, s2, lds, half);
+  const float n = (float)cols;
+  const float m1 = kind == kNormLayer ? s1 / n : 0.0f, m2 = s2 / n;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[c][j] = rs * (d[c][j] - m1 - h[c][j] * m2);
+}
+
+template <typename T, int NC, int W>
+__global__ __launch_bounds__((kThreads<W>), (kWaves<T, NC>)) void k_join_bwd(JoinBwd a) {
+  constexpr int V = kVec<T>, R = kRows<W>;
+  __shared__ float lds[2][2][kThreads<W> / 64];
+  int half = 0;
+  const int32_t cols = a.cols, groups = (cols + kAct8Group - 1) / kAct8Group;
+  const int32_t worker = blockIdx.y;
+  const int64_t base = (int64_t)worker * a.rows, stride = (int64_t)gridDim.x * R;
+  const RngKey key = load_key(a.drop);
+  int64_t i = (int64_t)blockIdx.x * R + threadIdx.x / (W * 64);
+  BwdRow<NC> next;
+  if (i < a.rows) load_bwd<T, NC, W>(a, base + i, groups, next);
+  float ga[NC][V], gc[NC][V];  // gamma; gate * gamma_b
+  params_or<T, NC, W>(a.gamma, cols, 1.0f, ga);
+  params_or<T, NC, W>(a.gate, cols, 1.0f, gc);
+  if (a.gamma_b) {
+    float t[NC][V];
+    load_params<T, NC, W>(a.gamma_b, cols, t);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) gc[c][j] *= t[c][j];
+  }
+  float sums[4][NC][V];
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) sums[s][c][j] = 0.0f;
+  for (int64_t i0 = (int64_t)blockIdx.x * R; i0 < a.rows; i0 += stride, i += stride) {
+    const bool in = i < a.rows;
+    const int64_t r = base + i;
+    float d[NC][V], dr[NC][V], h[NC][V], k[NC][V];
+    const float rs = next.rs, rsb = next.rsb;
+    const lu4 none = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int32_t col = chunk_col<T, W>(c);
+      unpack_row<T>(in && a.dz ? next.dz[c] : none, col, cols, d[c]);
+      unpack_row<T>(in && a.dr ? next.dr[c] : none, col, cols, dr[c]);
+      const float s = in && a.dz ? step_of(next.e[c]) : 0.0f;
+      const float sb = in && a.qb ? step_of(next.eb[c]) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        h[c][j] = in && a.dz ? dequant(next.q[c][j / 4], j % 4, s) : 0.0f;
+        k[c][j] = in && a.qb ? dequant(next.qb[c][j / 4], j % 4, sb) : 0.0f;
+      }
+    }
+    if (i + stride < a.rows) load_bwd<T, NC, W>(a, r + stride, groups, next);
+    if (a.dz) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          sums[0][c][j] = __builtin_fmaf(d[c][j], h[c][j], sums[0][c][j]);
+          sums[1][c][j] += d[c][j];
+          d[c][j] *= ga[c][j];
+        }
+      through<T, NC, W>(d, h, in ? rs : 0.0f, cols, a.kind, lds, half);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int32_t col = chunk_col<T, W>(c);
+      float o[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        d[c][j] = col + j < cols ? d[c][j] + dr[c][j] : 0.0f;
+        o[j] = a.alpha * d[c][j];
+      }
+      if (in && col < cols) store_row(static_cast<T*>(a.dx) + r * a.lddx, col, cols, o);
+      if (a.drop.threshold) drop<V>(a.drop, key, r, (cols + 7) / 8, col, d[c]);
+      if (a.qb) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          sums[2][c][j] = __builtin_fmaf(d[c][j], k[c][j], sums[2][c][j]);
+          sums[3][c][j] += d[c][j];
+        }
+      }
+    }
+    if (!a.db) continue;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[c][j] *= gc[c][j];
+    if (a.gamma_b) through<T, NC, W>(d, k, in ? rsb : 0.0f, cols, a.kind, lds, half);
+    if (!in) continue;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int32_t col = chunk_col<T, W>(c);
+      if (col < cols) store_row(static_cast<T*>(a.db) + r * a.lddb, col, cols, d[c]);
+    }
+  }
+  // the block's column sums: its rows add theirs in order
+  if (!a.part) return;
+  float* part = a.part + ((int64_t)worker * gridDim.x + blockIdx.x) * 4 * cols;
+  if constexpr (R > 1) {
+    __shared__ float all[4][NC * W * 64 * V];
+    for (int g = 0; g < R; ++g) {
+      if ((int)threadIdx.x / (W * 64) == g) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              const int32_t at = chunk_col<T, W>(c) + j;
+              all[s][at] = (g ? all[s][at] : 0.0f) + sums[s][c][j];
+            }
+      }
+      __syncthreads();
+    }
+    for (int32_t col = threadIdx.x; col < cols; col += kThreads<W>)
+      for (int s = 0; s < 4; ++s) part[s * cols + col] = all[s][col];
+  } else {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int32_t col = chunk_col<T, W>(c) + j;
+          if (col < cols) part[s * cols + col] = sums[s][c][j];
+        }
+  }
+}
+
+// The parameters' gradients of a worker from its blocks' partial sums, in
+// binary64: 64 columns to a block of 16 waves that each add every 16th partial,
+// joined in wave order.  blockIdx.z: the sums of the norm before the next block,
+// or those of the branch.
+constexpr int kJoinWaves = 16;
+template <typename G>
+__global__ __launch_bounds__(kJoinWaves * 64) void k_join_wgrad(JoinBwd a, int32_t blocks) {
+  __shared__ double lds[kJoinWaves][2][64];
+  const int32_t l = threadIdx.x & 63, w = threadIdx.x >> 6, col = blockIdx.x * 64 + l;
+  const int64_t cols = a.cols, worker = blockIdx.y;
+  const float* p = a.part + (worker * blocks * 4 + blockIdx.z * 2) * cols + col;
+  double s = 0.0, t = 0.0;
+  if (col < cols) {
+#pragma unroll 4
+    for (int32_t b = w; b < blocks; b += kJoinWaves) {
+      s += p[(int64_t)b * 4 * cols];
+      t += p[((int64_t)b * 4 + 1) * cols];
+    }
+  }
+  lds[w][0][l] = s;
+  lds[w][1][l] = t;
+  __syncthreads();
+  if (w > 0 || col >= cols) return;
+  s = t = 0.0;
+  for (int v = 0; v < kJoinWaves; ++v) {
+    s += lds[v][0][l];
+    t += lds[v][1][l];
+  }
+  const int64_t at = worker * a.ldg + col;
+  auto store = [&](void* to, double v) {
+    if (to) static_cast<G*>(to)[at] = (G)(float)v;
+  };
+  if (blockIdx.z == 0) {
+    store(a.dgamma, s);
+    store(a.dbeta, t);
+  } else {
+    const double gate = a.gate ? a.gate[col] : 1.0;
+    store(a.dgate, (a.gamma_b ? s * a.gamma_b[col] : s) + (a.beta_b ? t * a.beta_b[col] : 0.0));
+    store(a.dgamma_b, s * gate);
+    store(a.dbeta_b, t * gate);
+  }
+}
+
+// ---- launchers -------------------------------------------------------------------
+// One round of resident blocks, and no more than there are rows for.
+constexpr int64_t kResident = 512;  // blocks of 512 threads, 4 waves a SIMD
+
+template <typename T, int NC, int W>
+void fwd(const JoinFwd& a, hipStream_t st) {
+  const int64_t want = (a.rows + kRows<W> - 1) / kRows<W>;
+  const int64_t most = kResident * 512 / kThreads<W>;
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_join_fwd<T, NC, W>), dim3((uint32_t)std::min(want, most)),
+                     dim3(kThreads<W>), 0, st, a);
+}
+
+template <typename T, int NC, int W>
+void bwd(const JoinBwd& a, hipStream_t st) {
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_join_bwd<T, NC, W>),
+                     dim3(join_bwd_blocks(a.n, a.rows, a.cols), a.n), dim3(kThreads<W>), 0, st, a);
+}
+
+// The instance that holds a row: 8 columns a lane, 16 above 8192 columns.
+// Binary32 rows take twice the pieces (M).
+template <typename T, class A, class F>
+void pick(const A& a, F&& f) {
+  constexpr int M = 8 / kVec<T>;
+  if (a.cols <= 512) f(std::integral_constant<int, M>{}, std::integral_constant<int, 1>{});
+  else if (a.cols <= 1024) f(std::integral_constant<int, M>{}, std::integral_constant<int, 2>{});
+  else if (a.cols <= 2048) f(std::integral_constant<int, M>{}, std::integral_constant<int, 4>{});
+  else if (a.cols <= 4096) f(std::integral_constant<int, M>{}, std::integral_constant<int, 8>{});
+  else if (a.cols <= 8192) f(std::integral_constant<int, M>{}, std::integral_constant<int, 16>{});
+  else f(std::integral_constant<int, 2 * M>{}, std::integral_constant<int, 16>{});
+}
+
+template <typename T>
+void fwd(const JoinFwd& a, hipStream_t st) {
+  pick<T>(a, [&](auto nc, auto w) { fwd<T, nc.value, w.value>(a, st); });
+}
+template <typename T>
+void bwd(const JoinBwd& a, hipStream_t st) {
+  pick<T>(a, [&](auto nc, auto w) { bwd<T, nc.value, w.value>(a, st); });
+}
+
+template <typename G>
+void wgrad(const JoinBwd& a, hipStream_t st) {
+  const int32_t blocks = a.rows ? join_bwd_blocks(a.n, a.rows, a.cols) : 0;
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_join_wgrad<G>), dim3((a.cols + 63) / 64, a.n, 2),
+                     dim3(kJoinWaves * 64), 0, st, a, blocks);
+}
+
+}  // namespace
+
+int32_t join_bwd_blocks(int32_t n, int64_t rows, int32_t cols) {
+  const int64_t per = cols <= 512 ? 8 : cols <= 1024 ? 4 : cols <= 2048 ? 2 : 1;
+  const int64_t all = cols <= 4096 ? kResident : kResident / 2;
+  const int64_t most = std::max<int64_t>(1, all / n);
+  return (int32_t)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, most));
+}
+
+void launch_join(const JoinFwd& a, hipStream_t st) {
+  if (a.dtype == kGradF32) fwd<float>(a, st);
+  else if (a.dtype == kGradF16) fwd<_Float16>(a, st);
+  else fwd<__bf16>(a, st);
+}
+
+void launch_join_backward(const JoinBwd& a, hipStream_t st) {
+  if (a.dtype == kGradF32) bwd<float>(a, st);
+  else if (a.dtype == kGradF16) bwd<_Float16>(a, st);
+  else bwd<__bf16>(a, st);
+}
+
+void launch_join_weight_grad(const JoinBwd& a, hipStream_t st) {
+  if (a.g_dtype == kGradF32) wgrad<float>(a, st);
+  else if (a.g_dtype == kGradF16) wgrad<_Float16>(a, st);
+  else wgrad<__bf16>(a, st);
+}
+
+}  // namespace oba

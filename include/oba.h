@@ -493,6 +493,112 @@ int oba_linear_weight_grad(int32_t n, int64_t rows, int64_t in, int64_t out, con
                            void* db, int g_dtype, int64_t ldg, void* ws, size_t ws_bytes,
                            hipStream_t stream);
 
+/* ---- a gated feed-forward sub-layer -----------------------------------------
+ * What such a sub-layer computes beside the products above:
+ *   h = f(z wg^T + bg) * (z wu^T + bu)        oba_gated_linear
+ *   b = h w2^T + b2                           oba_linear
+ *   r = alpha x + gate * dropout(norm(b))     oba_residual_norm
+ *   z = norm(r), the next block's input       (the same call)
+ * The rules for matrices, parameters, gradients of n workers, workspaces and
+ * what may overlap are those of the layer calls above.
+ *
+ * Dropout.  An element's 16 random bits are a function of its row, its column,
+ * the seed, the step and the site, so no mask is stored and a backward pass
+ * gets the same one: Philox4x32 with 10 rounds (Salmon et al. 2011) on the
+ * counter words (i mod 2^32, i / 2^32, site, step mod 2^32), i = row *
+ * ceil(cols / 8) + col / 8, with the seed's two halves (low, high) as the key;
+ * column col has the lower (col even) or upper half of word (col % 8) / 2.  It
+ * is dropped if they are below t = rate * 65536, rounded to nearest, and else
+ * multiplied by 65536 / (65536 - t).  What is dropped is 0, whatever it was.
+ * rng: {seed, step} on the device, 8-byte aligned, read when the kernel runs: a
+ * captured step that adds 1 to the step draws another mask at each replay.
+ * site: tells the dropouts of one step apart.  rate: from 0, and t below 65536;
+ * where t is 0 nothing is dropped and rng may be NULL. */
+
+/* y = dropout(x) + add; on dy it is the backward pass.  add: or NULL. */
+int oba_dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dtype, double rate,
+                const uint64_t* rng, uint32_t site, const void* add, int64_t ldadd, void* y,
+                int64_t ldy, hipStream_t stream);
+
+/* Norms of rows: (v - mean) * rstd with rstd = 1 / sqrt(var + eta) as in
+ * oba_layer_norm, or v * rstd with rstd = 1 / sqrt(mean(v^2) + eta). */
+enum { OBA_NORM_LAYER = 0, OBA_NORM_RMS = 1 };
+
+/* What lies between two blocks:
+ *   n = norm(b) * gamma_b + beta_b           (gamma_b NULL: n = b)
+ *   r = alpha * x + gate * dropout(n)        (b NULL: r = alpha * x)
+ *   z = norm(r) * gamma + beta               (gamma NULL: none)
+ * x, b, r, z: rows of one dtype, at most 2^14 columns; z comes from r before it
+ * is rounded.  gate, beta_b, beta: or NULL (1, 0, 0).  r: or NULL if gamma is
+ * given.  rstd_b, rstd: [rows] binary32 out, with gamma_b and with gamma.  qb,
+ * eb: NULL, or norm(b) (b itself without gamma_b) kept in 8 bits; q, e: NULL, or
+ * norm(r).  Without b none of its arguments may be given, and without gamma_b or
+ * gamma none of theirs. */
+int oba_residual_norm(int64_t rows, int64_t cols, int dtype, int kind, double eta, const void* x,
+                      int64_t ldx, double alpha, const void* b, int64_t ldb, const float* gamma_b,
+                      const float* beta_b, const float* gate, double rate, const uint64_t* rng,
+                      uint32_t site, float* rstd_b, int8_t* qb, uint8_t* eb, void* r, int64_t ldr,
+                      const float* gamma, const float* beta, void* z, int64_t ldz, float* rstd,
+                      int8_t* q, uint8_t* e, hipStream_t stream);
+
+/* Its backward pass from what was kept, with h = norm(r), k = norm(b) (or b),
+ * a = dz * gamma:
+ *   D = rstd * (a - mean(a) - h * mean(a * h)) + dr     (mean(a): layer only)
+ *   dx = alpha * D,  v = dropout(D),  c = v * gate * gamma_b
+ *   db = rstd_b * (c - mean(c) - k * mean(c * k))       (gamma_b NULL: db = c)
+ * and for each of n workers dgamma = sum dz * h, dbeta = sum dz, dgamma_b = gate *
+ * sum v * k, dbeta_b = gate * sum v, dgate = sum v * (k * gamma_b + beta_b).
+ * gamma NULL: no norm of r, and dz, q, e, rstd NULL; dr: the gradient that r gets
+ * elsewhere, or NULL if gamma is given.  qb, eb: needed with gamma_b and for
+ * dgate.  db: or NULL.  The parameters' gradients: each or NULL.  ws: at least
+ * oba_residual_norm_backward_workspace_bytes(), 16-byte aligned (or NULL where
+ * all five are NULL). */
+size_t oba_residual_norm_backward_workspace_bytes(int32_t n, int64_t rows, int64_t cols);
+int oba_residual_norm_backward(int32_t n, int64_t rows, int64_t cols, int dtype, int kind,
+                               const void* dz, int64_t lddz, const int8_t* q, const uint8_t* e,
+                               const float* rstd, const float* gamma, const void* dr,
+                               int64_t lddr, double alpha, void* dx, int64_t lddx,
+                               const int8_t* qb, const uint8_t* eb, const float* rstd_b,
+                               const float* gamma_b, const float* beta_b, const float* gate,
+                               double rate, const uint64_t* rng, uint32_t site, void* db,
+                               int64_t lddb, void* dgamma, void* dbeta, void* dgamma_b,
+                               void* dbeta_b, void* dgate, int g_dtype, int64_t ldg, void* ws,
+                               size_t ws_bytes, hipStream_t stream);
+
+/* Gate functions f: the first four are the activation functions; p times the
+ * logistic function; the logistic function. */
+enum {
+  OBA_GATE_NONE = 0,
+  OBA_GATE_RELU = 1,
+  OBA_GATE_GELU = 2,
+  OBA_GATE_GELU_TANH = 3,
+  OBA_GATE_SILU = 4,
+  OBA_GATE_SIGMOID = 5
+};
+
+/* p = x wg^T + bg, u = x wu^T + bu, y = f(p) * u.  x: [rows][in]; w:
+ * [2*hidden][in], wg its first hidden rows and wu the others; bias: [2*hidden]
+ * likewise, or NULL; y: [rows][hidden]; dtype OBA_F16 or OBA_BF16, 2*hidden at
+ * most 2^20.  qp, ep, qu, eu: NULL, or p and u kept in 8 bits for the backward
+ * pass (from their binary32 values).  q, e: NULL, or y in 8 bits, as
+ * oba_act8_encode makes them of it.  ws: at least
+ * oba_gated_linear_workspace_bytes(), 16-byte aligned (NULL if that is 0). */
+size_t oba_gated_linear_workspace_bytes(int64_t rows, int64_t in, int64_t hidden);
+int oba_gated_linear(int64_t rows, int64_t in, int64_t hidden, const void* x, int64_t ldx,
+                     const void* w, int64_t ldw, int dtype, const float* bias, int gate, void* y,
+                     int64_t ldy, int8_t* qp, uint8_t* ep, int8_t* qu, uint8_t* eu, int8_t* q,
+                     uint8_t* e, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Back through the product that reads y (w: [out][hidden]) and through the gate,
+ * with d = dy w:  dpu = [d * u * f'(p), d * f(p)], [rows][2*hidden].  With
+ * oba_linear_input_grad and oba_linear_weight_grad of 2*hidden outputs it gives
+ * the gradients of x, w and bias.  dy: [rows][out]; p, u: as kept. */
+size_t oba_gated_hidden_grad_workspace_bytes(int64_t rows, int64_t hidden, int64_t out);
+int oba_gated_hidden_grad(int64_t rows, int64_t hidden, int64_t out, const void* dy, int64_t lddy,
+                          const void* w, int64_t ldw, int dtype, int gate, const int8_t* qp,
+                          const uint8_t* ep, const int8_t* qu, const uint8_t* eu, void* dpu,
+                          int64_t lddpu, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---- kernel timing (measurement aid) ---------------------------------------
  * While enabled, every kernel the library launches is bracketed by two HIP
  * events on the launch stream (up to `capacity` launches are kept).
@@ -503,8 +609,9 @@ int oba_linear_weight_grad(int32_t n, int64_t rows, int64_t in, int64_t out, con
  * "freeze_variance", "compress_deferred", "server_deferred",
  * "deferred_errors", "server_momentum", "compress_deferred_local",
  * "step_small", "act8_encode", "act8_decode", "layer_norm",
- * "layer_norm_backward", "linear", "linear_input_grad", "linear_weight_grad"
- * (each of these one record per call, all of its kernels in it); the listed entry points record under the names of their flat
+ * "layer_norm_backward", "linear", "linear_input_grad", "linear_weight_grad",
+ * "dropout", "residual_norm", "residual_norm_backward", "gated_linear",
+ * "gated_hidden_grad" (each of these one record per call, all of its kernels in it); the listed entry points record under the names of their flat
  * forms; "adam_warmup" includes the norm kernel of
  * oba_adam_warmup_step_vnorm).  oba_timing_reset drops all records. */
 int oba_timing_enable(int on, int32_t capacity);
