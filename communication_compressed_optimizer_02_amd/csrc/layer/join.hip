@@ -36,6 +36,27 @@ namespace oba {
 
 namespace {
 
+// A pointer that came out of memory, as one to global memory.
+template <typename P>
+__device__ __forceinline__ P* global(P* p) {
+  return (P*)(__attribute__((address_space(1))) P*)p;
+}
+
+// The kernel's argument block, read again where it is asked for: its 30 pointers
+// and strides do not fit the scalar registers together, and kept for all of a
+// kernel they spilled (46 scalar registers, and vector registers to hold them).
+template <typename A>
+__device__ __forceinline__ A arguments(const A& a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef const __attribute__((address_space(4))) A* Block;
+  Block p = (Block)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *p;
+#else
+  return a;
+#endif
+}
+
 // W waves to a row; blocks of 8 waves hold 8 / W rows at a time, 16 waves one.
 template <int W>
 constexpr int kThreads = W == 16 ? 1024 : 512;
@@ -58,6 +79,7 @@ __device__ __forceinline__ void row_sums(F& a, F& b, F (*lds)[2][kThreads<W> / 6
     }
     __syncthreads();
     a = b = 0;
+#pragma unroll 4
     for (int i = 0; i < W; ++i) {
       a += lds[half][0][first + i];
       b += lds[half][1][first + i];
@@ -75,61 +97,85 @@ __device__ __forceinline__ int32_t wave_cols(int32_t w, int32_t cols) {
   return n;
 }
 
+// The sum of a lane's columns.  Binary32 rows are added in binary64: a binary32
+// sum is off by the rounding of values of the mean's size, which the normalised
+// row has in units of its spread.  16-bit rows are added in binary32: eight
+// values of at most 11 bits are exact there unless one is below 2^-10 of the
+// largest, and then the spread is no smaller than a share of the largest; a
+// rounded r is off by as much itself.
+template <typename T, int NC>
+__device__ __forceinline__ double lane_sum(const float (&v)[NC][kVec<T>]) {
+  constexpr int V = kVec<T>;
+  double s = 0.0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if constexpr (V == 4) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) s += (double)v[c][j];
+    } else {
+      s += (double)(((v[c][0] + v[c][1]) + (v[c][2] + v[c][3])) +
+                    ((v[c][4] + v[c][5]) + (v[c][6] + v[c][7])));
+    }
+  }
+  return s;
+}
+
 // Rows to their normalised form in place; the reciprocal of the spread.  The
-// mean comes from binary64 sums (a binary32 one is off by the rounding of values
-// of the mean's size), the squares from values centred on their wave's mean; the
-// waves' squares are moved to the row's mean, n_w (mean_w - mean)^2 each, so one
-// exchange serves both.  Quotients are put right by their remainders: a constant
-// row's mean is its value.
+// squares are of values centred on their wave's mean and are moved to the row's,
+// n_w (mean_w - mean)^2 for each wave, so that one exchange between the waves
+// serves mean and spread.  Quotients are put right by their remainders: a
+// constant row's mean is its value.
 template <typename T, int NC, int W>
 __device__ __forceinline__ float normalise(float (&v)[NC][kVec<T>], int32_t cols, int kind,
                                            float eta, double (*lds)[2][kThreads<W> / 64],
                                            int& half) {
   constexpr int V = kVec<T>;
-  double mean = 0.0, squares;
+  const int wave = threadIdx.x >> 6, first = wave & ~(W - 1);
+  double squares;
+  float mu = 0.0f, off = 0.0f;
   if (kind == kNormLayer) {
-    double s = 0.0;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < V; ++j) s += (double)v[c][j];
-    s = wave_sum(s);
     auto quotient = [](double s, double n) {
       const double inv = n > 0.0 ? 1.0 / n : 0.0, m = s * inv;
       return __builtin_fma(__builtin_fma(-m, n, s), inv, m);
     };
-    const int w = W == 1 ? 0 : (int)(threadIdx.x >> 6) & (W - 1);
-    mean = quotient(s, (double)wave_cols<T, NC, W>(w, cols));
-    const float mu = (float)mean, off = (float)(mean - (double)mu);
+    const double s = wave_sum(lane_sum<T, NC>(v));
+    double mean = quotient(s, (double)wave_cols<T, NC, W>(wave & (W - 1), cols));
+    mu = (float)mean;
     float s2 = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      float t[V];
+      // lanes that hold none of the row, and elements past its end, add nothing
+      const int32_t col = chunk_col<T, W>(c);
+      const float m = col < cols ? mu : 0.0f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) t[j] = v[c][j];
-      centre(t, mu, off, chunk_col<T, W>(c), cols);
-#pragma unroll
-      for (int j = 0; j < V; ++j) s2 = __builtin_fmaf(t[j], t[j], s2);
+      for (int j = 0; j < V; ++j) {
+        float t = v[c][j] - m;
+        if (cols % V != 0) t = col + j < cols ? t : 0.0f;
+        s2 = __builtin_fmaf(t, t, s2);
+      }
     }
     squares = (double)wave_sum(s2);
     if constexpr (W > 1) {
-      const int wave = threadIdx.x >> 6, first = wave & ~(W - 1);
       if ((threadIdx.x & 63) == 0) {
         lds[half][0][wave] = s;
         lds[half][1][wave] = squares;
       }
       __syncthreads();
-      s = 0.0;
-      for (int i = 0; i < W; ++i) s += lds[half][0][first + i];
-      mean = quotient(s, (double)cols);
+      double all = 0.0;
+#pragma unroll 4
+      for (int i = 0; i < W; ++i) all += lds[half][0][first + i];
+      mean = quotient(all, (double)cols);
       squares = 0.0;
+#pragma unroll 2
       for (int i = 0; i < W; ++i) {
         const double n = (double)wave_cols<T, NC, W>(i, cols);
         const double d = quotient(lds[half][0][first + i], n) - mean;
         squares += n > 0.0 ? __builtin_fma(n * d, d, lds[half][1][first + i]) : 0.0;
       }
       half ^= 1;
+      mu = (float)mean;
     }
+    off = (float)(mean - (double)mu);
   } else {
     float s2 = 0.0f;
 #pragma unroll
@@ -139,21 +185,32 @@ __device__ __forceinline__ float normalise(float (&v)[NC][kVec<T>], int32_t cols
     s2 = wave_sum(s2);
     squares = (double)s2;
     if constexpr (W > 1) {
-      const int wave = threadIdx.x >> 6, first = wave & ~(W - 1);
       if ((threadIdx.x & 63) == 0) lds[half][0][wave] = squares;
       __syncthreads();
       squares = 0.0;
+#pragma unroll 4
       for (int i = 0; i < W; ++i) squares += lds[half][0][first + i];
       half ^= 1;
     }
   }
   const float rs = 1.0f / __builtin_sqrtf((float)(squares / (double)cols) + eta);
-  const float mu = (float)mean, off = (float)(mean - (double)mu);
+  if (kind == kNormLayer) {
+    const float low = -off * rs;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    if (kind == kNormLayer) centre(v[c], mu, off, chunk_col<T, W>(c), cols);
+    for (int c = 0; c < NC; ++c) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[c][j] *= rs;
+      for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(v[c][j] - mu, rs, low);
+      if (cols % (NC * W * 64 * V) != 0) {  // 0 stays past the row's end
+        const int32_t col = chunk_col<T, W>(c);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[c][j] = col + j < cols ? v[c][j] : 0.0f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[c][j] *= rs;
   }
   return rs;
 }
@@ -164,8 +221,12 @@ __device__ __forceinline__ void keep(const float (&v)[kVec<T>], int8_t* q, uint8
                                      int32_t groups, int32_t col) {
   constexpr int V = kVec<T>;
   uint32_t top = 0;
+  if constexpr (V == 8) {
+    top = magnitude8(v);
+  } else {
 #pragma unroll
-  for (int j = 0; j < V; ++j) top = max(top, magnitude(v[j]));
+    for (int j = 0; j < V; ++j) top = max(top, magnitude(v[j]));
+  }
   top = max_lanes<kAct8Group / V>(top);
   const uint32_t ex = group_exp(top);
   const float inv = inv_step_of(ex), step = step_of(ex);
@@ -179,25 +240,64 @@ __device__ __forceinline__ void keep(const float (&v)[kVec<T>], int8_t* q, uint8
   if (col % kAct8Group == 0) e[row * groups + col / kAct8Group] = (uint8_t)ex;
 }
 
+// A parameter vector's columns in a lane, `other` where there is no vector; 0
+// past the last column.  Rows of 8 columns a lane hold them in registers from row
+// to row; at 16 columns a lane they are read again for each row (from cache): held
+// they spilled.
 template <typename T, int NC, int W>
-__device__ __forceinline__ void params_or(const float* p, int32_t cols, float other,
-                                          float (&v)[NC][kVec<T>]) {
-  if (p) {
-    load_params<T, NC, W>(p, cols, v);
-  } else {
+struct Params {
+  static constexpr int V = kVec<T>;
+  static constexpr bool kHold = NC * V <= 8;
+  const float* p;
+  float other;
+  float held[kHold ? NC : 1][V];
+
+  __device__ __forceinline__ void read(int c, int32_t cols, float (&v)[V]) const {
+    const int32_t col = chunk_col<T, W>(c);
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < kVec<T>; ++j) v[c][j] = other;
+    for (int j = 0; j < V; j += 4) {
+      if (!p) {
+        for (int i = 0; i < 4; ++i) v[j + i] = other;
+      } else if (col + j + 4 <= cols) {
+        const Four f = *reinterpret_cast<const Four*>(p + col + j);
+        for (int i = 0; i < 4; ++i) v[j + i] = f.v[i];
+      } else {
+        for (int i = 0; i < 4; ++i) v[j + i] = col + j + i < cols ? p[col + j + i] : 0.0f;
+      }
+    }
   }
+  __device__ __forceinline__ Params(const float* from, float without, int32_t cols)
+      : p(from), other(without) {
+    if constexpr (kHold) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) read(c, cols, held[c]);
+    }
+  }
+  __device__ __forceinline__ void get(int c, int32_t cols, float (&v)[V]) const {
+    if constexpr (kHold) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = held[c][j];
+    } else {
+      read(c, cols, v);
+    }
+  }
+};
+
+// Waves per SIMD asked of the compiler.  A row of 16 columns a lane has 16 waves
+// in a block, so four to a SIMD too; its loads are not a row ahead, which spilled.
+constexpr int kWaves = 4;
+template <typename T, int NC>
+constexpr bool kAhead = NC * kVec<T> <= 8;
+
+// The row of a block's first round that a wave belongs to, the same for all its
+// lanes: addresses of rows then need no vector registers.
+template <int W>
+__device__ __forceinline__ int32_t wave_row() {
+  return __builtin_amdgcn_readfirstlane((int32_t)threadIdx.x / (W * 64));
 }
 
-// Waves per SIMD asked of the compiler.
-template <typename T, int NC>
-constexpr int kWaves = NC * kVec<T> <= 8 ? 4 : 2;
-
 template <typename T, int NC, int W>
-__global__ __launch_bounds__((kThreads<W>), (kWaves<T, NC>)) void k_join_fwd(JoinFwd a) {
+__global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_fwd(JoinFwd a) {
   constexpr int V = kVec<T>, R = kRows<W>;
   __shared__ double lds[2][2][kThreads<W> / 64];
   int half = 0;
@@ -205,35 +305,30 @@ __global__ __launch_bounds__((kThreads<W>), (kWaves<T, NC>)) void k_join_fwd(Joi
   const int64_t stride = (int64_t)gridDim.x * R;
   const bool first_lane = (threadIdx.x & (W * 64 - 1)) == 0;
   const RngKey key = load_key(a.drop);
-  int64_t r = (int64_t)blockIdx.x * R + threadIdx.x / (W * 64);
-  // a row ahead: its loads are in flight while this one is worked on
+  int64_t r = (int64_t)blockIdx.x * R + wave_row<W>();
+  constexpr bool A = kAhead<T, NC>;  // each loaded anew once the row before is taken out of it
   lu4 nx[NC], nb[NC];
-  auto load = [&](int64_t row) {
+  auto load = [&](const void* from, int64_t ld, int64_t row, lu4 (&to)[NC]) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int32_t col = chunk_col<T, W>(c);
-      nx[c] = load_raw(static_cast<const T*>(a.x) + row * a.ldx, col, cols);
-      if (a.b) nb[c] = load_raw(static_cast<const T*>(a.b) + row * a.ldb, col, cols);
-    }
+    for (int c = 0; c < NC; ++c)
+      to[c] = load_raw(static_cast<const T*>(from) + row * ld, chunk_col<T, W>(c), cols);
   };
-  if (r < a.rows) load(r);
-  float gate[NC][V], gb[NC][V], bb[NC][V], ga[NC][V], be[NC][V];
-  params_or<T, NC, W>(a.gate, cols, 1.0f, gate);
-  params_or<T, NC, W>(a.gamma_b, cols, 1.0f, gb);
-  params_or<T, NC, W>(a.beta_b, cols, 0.0f, bb);
-  params_or<T, NC, W>(a.gamma, cols, 1.0f, ga);
-  params_or<T, NC, W>(a.beta, cols, 0.0f, be);
+  if (A && r < a.rows) {
+    load(a.x, a.ldx, r, nx);
+    if (a.b) load(a.b, a.ldb, r, nb);
+  }
+  const Params<T, NC, W> gate(a.gate, 1.0f, cols), gb(a.gamma_b, 1.0f, cols),
+      bb(a.beta_b, 0.0f, cols), ga(a.gamma, 1.0f, cols), be(a.beta, 0.0f, cols);
   // the rows of a block go round together: its waves meet at the sums' barriers
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += stride, r += stride) {
-    const bool in = r < a.rows;
-    float x[NC][V], v[NC][V];
+    const bool in = r < a.rows, more = r + stride < a.rows;
+    const lu4 none = {0u, 0u, 0u, 0u};
+    float v[NC][V];
+    if (!A && a.b && in) load(a.b, a.ldb, r, nb);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int32_t col = chunk_col<T, W>(c);
-      unpack_row<T>(in ? nx[c] : lu4{0u, 0u, 0u, 0u}, col, cols, x[c]);
-      unpack_row<T>(in && a.b ? nb[c] : lu4{0u, 0u, 0u, 0u}, col, cols, v[c]);
-    }
-    if (r + stride < a.rows) load(r + stride);
+    for (int c = 0; c < NC; ++c)
+      unpack_row<T>(in && a.b ? nb[c] : none, chunk_col<T, W>(c), cols, v[c]);
+    if (A && a.b && more) load(a.b, a.ldb, r + stride, nb);
     if (a.b) {
       if (a.gamma_b) {
         const float rs = normalise<T, NC, W>(v, cols, a.kind, a.eta, lds, half);
@@ -245,41 +340,56 @@ __global__ __launch_bounds__((kThreads<W>), (kWaves<T, NC>)) void k_join_fwd(Joi
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
+        float f[V], o[V];
         if (a.gamma_b) {
+          gb.get(c, cols, f);
+          bb.get(c, cols, o);
 #pragma unroll
-          for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(v[c][j], gb[c][j], bb[c][j]);
+          for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(v[c][j], f[j], o[j]);
         }
         if (a.drop.threshold) drop<V>(a.drop, key, r, (cols + 7) / 8, chunk_col<T, W>(c), v[c]);
         if (a.gate) {
+          gate.get(c, cols, f);
 #pragma unroll
-          for (int j = 0; j < V; ++j) v[c][j] *= gate[c][j];
+          for (int j = 0; j < V; ++j) v[c][j] *= f[j];
         }
       }
     }
+    if (!A && in) load(a.x, a.ldx, r, nx);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float x[V];
+      unpack_row<T>(in ? nx[c] : none, chunk_col<T, W>(c), cols, x);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(a.alpha, x[j], v[c][j]);
+    }
+    if (A && more) load(a.x, a.ldx, r + stride, nx);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
-#pragma unroll
-      for (int j = 0; j < V; ++j) x[c][j] = __builtin_fmaf(a.alpha, x[c][j], v[c][j]);
-      if (a.r && in && col < cols) store_row(static_cast<T*>(a.r) + r * a.ldr, col, cols, x[c]);
+      if (a.r && in && col < cols) store_row(static_cast<T*>(a.r) + r * a.ldr, col, cols, v[c]);
     }
     if (!a.gamma) continue;
-    const float rs = normalise<T, NC, W>(x, cols, a.kind, a.eta, lds, half);
+    const float rs = normalise<T, NC, W>(v, cols, a.kind, a.eta, lds, half);
     if (!in) continue;
     if (first_lane) a.rstd[r] = rs;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
-      if (a.q) keep<T>(x[c], a.q, a.e, r, groups, col);
+      if (a.q) keep<T>(v[c], a.q, a.e, r, groups, col);
+      float f[V], o[V];
+      ga.get(c, cols, f);
+      be.get(c, cols, o);
 #pragma unroll
-      for (int j = 0; j < V; ++j) x[c][j] = __builtin_fmaf(x[c][j], ga[c][j], be[c][j]);
-      if (col < cols) store_row(static_cast<T*>(a.z) + r * a.ldz, col, cols, x[c]);
+      for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(v[c][j], f[j], o[j]);
+      if (col < cols) store_row(static_cast<T*>(a.z) + r * a.ldz, col, cols, v[c]);
     }
   }
 }
 
 // ---- backward ------------------------------------------------------------------
-// What a row's backward pass reads, as it lies in memory.
+// What a row's backward pass reads, as it lies in memory, a row ahead: each half
+// is loaded anew as soon as the row before has been taken out of it.
 template <int NC>
 struct BwdRow {
   lu4 dz[NC], dr[NC];
@@ -302,24 +412,47 @@ __device__ __forceinline__ void load_kept(const int8_t* q, const uint8_t* e, int
   }
 }
 
-template <typename T, int NC, int W>
-__device__ __forceinline__ void load_bwd(const JoinBwd& a, int64_t r, int32_t groups,
-                                         BwdRow<NC>& w) {
-  if (a.dz) w.rs = a.rstd[r];
-  if (a.gamma_b) w.rsb = a.rstd_b[r];
+// The values: a byte with its sign bit turned over is the integer plus 128, which
+// converts in one instruction; (u - 128) * step is exact in one more.  0 where
+// there are none.
+template <typename T>
+__device__ __forceinline__ void decode(bool there, lu2 q, uint32_t e, float (&v)[kVec<T>]) {
+  const float step = there ? step_of(e) : 0.0f, low = -128.0f * step;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int32_t col = chunk_col<T, W>(c);
-    if (a.dz) {
-      w.dz[c] = load_raw(static_cast<const T*>(a.dz) + r * a.lddz, col, a.cols);
-      load_kept<T>(a.q, a.e, r, groups, col, a.cols, w.q[c], w.e[c]);
-    }
-    if (a.dr) w.dr[c] = load_raw(static_cast<const T*>(a.dr) + r * a.lddr, col, a.cols);
-    if (a.qb) load_kept<T>(a.qb, a.eb, r, groups, col, a.cols, w.qb[c], w.eb[c]);
+  for (int j = 0; j < kVec<T>; ++j) {
+    const uint32_t w = q[j / 4] ^ 0x80808080u;
+    v[j] = __builtin_fmaf((float)((w >> (8 * (j % 4))) & 0xFFu), step, low);
   }
 }
 
-// The norm's input gradient from that of its normalised rows, in place.
+template <typename T, int NC, int W>
+__device__ __forceinline__ void load_upper(const JoinBwd& a, int64_t r, BwdRow<NC>& w) {
+  if (!a.dz) return;
+  const int32_t groups = (a.cols + kAct8Group - 1) / kAct8Group;
+  w.rs = global(a.rstd)[r];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int32_t col = chunk_col<T, W>(c);
+    w.dz[c] = load_raw(global(static_cast<const T*>(a.dz)) + r * a.lddz, col, a.cols);
+    load_kept<T>(global(a.q), global(a.e), r, groups, col, a.cols, w.q[c], w.e[c]);
+  }
+}
+
+template <typename T, int NC, int W>
+__device__ __forceinline__ void load_lower(const JoinBwd& a, int64_t r, BwdRow<NC>& w) {
+  const int32_t groups = (a.cols + kAct8Group - 1) / kAct8Group;
+  if (a.gamma_b) w.rsb = global(a.rstd_b)[r];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int32_t col = chunk_col<T, W>(c);
+    if (a.dr) w.dr[c] = load_raw(global(static_cast<const T*>(a.dr)) + r * a.lddr, col, a.cols);
+    if (a.qb) load_kept<T>(global(a.qb), global(a.eb), r, groups, col, a.cols, w.qb[c], w.eb[c]);
+  }
+}
+
+// The norm's input gradient from that of its normalised rows, in place.  What it
+// leaves past a row's end reaches no result: the sums of the branch there are not
+// stored, and the parameters, 0 there, keep it out of the next row sums.
 template <typename T, int NC, int W>
 __device__ __forceinline__ void through(float (&d)[NC][kVec<T>], const float (&h)[NC][kVec<T>],
                                         float rs, int32_t cols, int kind,
@@ -335,36 +468,32 @@ __device__ __forceinline__ void through(float (&d)[NC][kVec<T>], const float (&h
     }
   row_sums<W>(s1, s2, lds, half);
   const float n = (float)cols;
-  const float m1 = kind == kNormLayer ? s1 / n : 0.0f, m2 = s2 / n;
+  const float m1 = kind == kNormLayer ? -rs * (s1 / n) : 0.0f, m2 = -s2 / n;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int j = 0; j < V; ++j) d[c][j] = rs * (d[c][j] - m1 - h[c][j] * m2);
+    for (int j = 0; j < V; ++j)
+      d[c][j] = __builtin_fmaf(__builtin_fmaf(m2, h[c][j], d[c][j]), rs, m1);
 }
 
 template <typename T, int NC, int W>
-__global__ __launch_bounds__((kThreads<W>), (kWaves<T, NC>)) void k_join_bwd(JoinBwd a) {
+__global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_bwd(JoinBwd args) {
+  JoinBwd a = arguments(args);
   constexpr int V = kVec<T>, R = kRows<W>;
   __shared__ float lds[2][2][kThreads<W> / 64];
   int half = 0;
-  const int32_t cols = a.cols, groups = (cols + kAct8Group - 1) / kAct8Group;
-  const int32_t worker = blockIdx.y;
-  const int64_t base = (int64_t)worker * a.rows, stride = (int64_t)gridDim.x * R;
+  const int32_t cols = a.cols, worker = blockIdx.y;
+  const int64_t rows = a.rows, base = worker * rows, stride = (int64_t)gridDim.x * R;
   const RngKey key = load_key(a.drop);
-  int64_t i = (int64_t)blockIdx.x * R + threadIdx.x / (W * 64);
+  int64_t i = (int64_t)blockIdx.x * R + wave_row<W>();
+  constexpr bool A = kAhead<T, NC>;
   BwdRow<NC> next;
-  if (i < a.rows) load_bwd<T, NC, W>(a, base + i, groups, next);
-  float ga[NC][V], gc[NC][V];  // gamma; gate * gamma_b
-  params_or<T, NC, W>(a.gamma, cols, 1.0f, ga);
-  params_or<T, NC, W>(a.gate, cols, 1.0f, gc);
-  if (a.gamma_b) {
-    float t[NC][V];
-    load_params<T, NC, W>(a.gamma_b, cols, t);
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < V; ++j) gc[c][j] *= t[c][j];
+  if (A && i < rows) {
+    load_upper<T, NC, W>(a, base + i, next);
+    load_lower<T, NC, W>(a, base + i, next);
   }
+  const Params<T, NC, W> ga(global(a.gamma), 1.0f, cols), gate(global(a.gate), 1.0f, cols),
+      gb(global(a.gamma_b), 1.0f, cols);
   float sums[4][NC][V];
 #pragma unroll
   for (int s = 0; s < 4; ++s)
@@ -372,72 +501,91 @@ __global__ __launch_bounds__((kThreads<W>), (kWaves<T, NC>)) void k_join_bwd(Joi
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) sums[s][c][j] = 0.0f;
-  for (int64_t i0 = (int64_t)blockIdx.x * R; i0 < a.rows; i0 += stride, i += stride) {
-    const bool in = i < a.rows;
+  for (int64_t i0 = (int64_t)blockIdx.x * R; i0 < rows; i0 += stride, i += stride) {
+    const bool in = i < rows, more = i + stride < rows;
     const int64_t r = base + i;
-    float d[NC][V], dr[NC][V], h[NC][V], k[NC][V];
-    const float rs = next.rs, rsb = next.rsb;
     const lu4 none = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int32_t col = chunk_col<T, W>(c);
-      unpack_row<T>(in && a.dz ? next.dz[c] : none, col, cols, d[c]);
-      unpack_row<T>(in && a.dr ? next.dr[c] : none, col, cols, dr[c]);
-      const float s = in && a.dz ? step_of(next.e[c]) : 0.0f;
-      const float sb = in && a.qb ? step_of(next.eb[c]) : 0.0f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        h[c][j] = in && a.dz ? dequant(next.q[c][j / 4], j % 4, s) : 0.0f;
-        k[c][j] = in && a.qb ? dequant(next.qb[c][j / 4], j % 4, sb) : 0.0f;
-      }
-    }
-    if (i + stride < a.rows) load_bwd<T, NC, W>(a, r + stride, groups, next);
+    float d[NC][V];
+    a = arguments(args);
+    if (!A && in) load_upper<T, NC, W>(a, r, next);
     if (a.dz) {
+      float h[NC][V];
+      const float rs = in ? next.rs : 0.0f;
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+      for (int c = 0; c < NC; ++c) {
+        unpack_row<T>(in ? next.dz[c] : none, chunk_col<T, W>(c), cols, d[c]);
+        decode<T>(in, next.q[c], next.e[c], h[c]);
+      }
+      if (A && more) load_upper<T, NC, W>(a, r + stride, next);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float f[V];
+        ga.get(c, cols, f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           sums[0][c][j] = __builtin_fmaf(d[c][j], h[c][j], sums[0][c][j]);
           sums[1][c][j] += d[c][j];
-          d[c][j] *= ga[c][j];
+          d[c][j] *= f[j];
         }
-      through<T, NC, W>(d, h, in ? rs : 0.0f, cols, a.kind, lds, half);
+      }
+      through<T, NC, W>(d, h, rs, cols, a.kind, lds, half);
+    } else {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < V; ++j) d[c][j] = 0.0f;
     }
+    a = arguments(args);
+    if (!A && in) load_lower<T, NC, W>(a, r, next);
+    float k[NC][V];
+    const float rsb = in ? next.rsb : 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (a.dr) {
+        float o[V];
+        unpack_row<T>(in ? next.dr[c] : none, chunk_col<T, W>(c), cols, o);
+#pragma unroll
+        for (int j = 0; j < V; ++j) d[c][j] += o[j];
+      }
+      decode<T>(in && a.qb, next.qb[c], next.eb[c], k[c]);
+    }
+    if (A && more) load_lower<T, NC, W>(a, r + stride, next);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
       float o[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        d[c][j] = col + j < cols ? d[c][j] + dr[c][j] : 0.0f;
-        o[j] = a.alpha * d[c][j];
-      }
-      if (in && col < cols) store_row(static_cast<T*>(a.dx) + r * a.lddx, col, cols, o);
+      for (int j = 0; j < V; ++j) o[j] = a.alpha * d[c][j];
+      if (in && col < cols) store_row(global(static_cast<T*>(a.dx)) + r * a.lddx, col, cols, o);
       if (a.drop.threshold) drop<V>(a.drop, key, r, (cols + 7) / 8, col, d[c]);
-      if (a.qb) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          sums[2][c][j] = __builtin_fmaf(d[c][j], k[c][j], sums[2][c][j]);
-          sums[3][c][j] += d[c][j];
-        }
+      for (int j = 0; j < V; ++j) {
+        sums[2][c][j] = __builtin_fmaf(d[c][j], k[c][j], sums[2][c][j]);
+        sums[3][c][j] += d[c][j];
+      }
+      if (a.gate) {
+        gate.get(c, cols, o);
+#pragma unroll
+        for (int j = 0; j < V; ++j) d[c][j] *= o[j];
+      }
+      if (a.gamma_b) {
+        gb.get(c, cols, o);
+#pragma unroll
+        for (int j = 0; j < V; ++j) d[c][j] *= o[j];
       }
     }
     if (!a.db) continue;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < V; ++j) d[c][j] *= gc[c][j];
-    if (a.gamma_b) through<T, NC, W>(d, k, in ? rsb : 0.0f, cols, a.kind, lds, half);
+    if (a.gamma_b) through<T, NC, W>(d, k, rsb, cols, a.kind, lds, half);
     if (!in) continue;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
-      if (col < cols) store_row(static_cast<T*>(a.db) + r * a.lddb, col, cols, d[c]);
+      if (col < cols) store_row(global(static_cast<T*>(a.db)) + r * a.lddb, col, cols, d[c]);
     }
   }
   // the block's column sums: its rows add theirs in order
   if (!a.part) return;
-  float* part = a.part + ((int64_t)worker * gridDim.x + blockIdx.x) * 4 * cols;
+  float* part = global(a.part) + ((int64_t)worker * gridDim.x + blockIdx.x) * 4 * cols;
   if constexpr (R > 1) {
     __shared__ float all[4][NC * W * 64 * V];
     for (int g = 0; g < R; ++g) {
