@@ -97,84 +97,114 @@ __device__ __forceinline__ int32_t wave_cols(int32_t w, int32_t cols) {
   return n;
 }
 
-// The sum of a lane's columns.  Binary32 rows are added in binary64: a binary32
-// sum is off by the rounding of values of the mean's size, which the normalised
-// row has in units of its spread.  16-bit rows are added in binary32: eight
-// values of at most 11 bits are exact there unless one is below 2^-10 of the
-// largest, and then the spread is no smaller than a share of the largest; a
-// rounded r is off by as much itself.
-template <typename T, int NC>
-__device__ __forceinline__ double lane_sum(const float (&v)[NC][kVec<T>]) {
+// What a norm divides by: columns of the row and of the lane's wave, with their
+// reciprocals, which a division for each row would cost 20 instructions of
+// binary64.  A quotient by a reciprocal is put right by its remainder.
+struct Share {
+  double n, inv;
+};
+__device__ __forceinline__ Share share_of(int32_t n) {
+  auto uniform = [](double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)u);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  };
+  return Share{uniform((double)n), uniform(n > 0 ? 1.0 / (double)n : 0.0)};
+}
+__device__ __forceinline__ double quotient(double s, double n, double inv) {
+  const double m = s * inv;
+  return __builtin_fma(__builtin_fma(-m, n, s), inv, m);
+}
+__device__ __forceinline__ float quotient(float s, float n, float inv) {
+  const float m = s * inv;
+  return __builtin_fmaf(__builtin_fmaf(-m, n, s), inv, m);
+}
+
+// The mean and the squares around it of the columns that a wave holds.  The sums
+// are taken twice, the second time around the first one's mean m, so that the mean
+// and the squares are off by what rounds differences, not values: m + sum(v - m) /
+// n.  For binary32 rows the first sum is binary64 and the second needs no mean:
+// a row of one value, whose sum binary32 does not hold, is then centred to 0.  For
+// 16-bit rows (and r made of them) binary32 does.
+template <typename T, int NC, int W>
+__device__ __forceinline__ void wave_moments(const float (&v)[NC][kVec<T>], int32_t cols,
+                                             const Share& part, double& mean, double& squares) {
   constexpr int V = kVec<T>;
-  double s = 0.0;
+  float m;
+  if constexpr (V == 4) {
+    double s = 0.0;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    if constexpr (V == 4) {
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) s += (double)v[c][j];
-    } else {
-      s += (double)(((v[c][0] + v[c][1]) + (v[c][2] + v[c][3])) +
-                    ((v[c][4] + v[c][5]) + (v[c][6] + v[c][7])));
+    mean = quotient(wave_sum(s), part.n, part.inv);
+    m = (float)mean;
+  } else {
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) s += v[c][j];
+    m = quotient(wave_sum(s), (float)part.n, (float)part.inv);
+  }
+  float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    // lanes that hold none of the row, and elements past its end, add nothing
+    const int32_t col = chunk_col<T, W>(c);
+    const float mc = col < cols ? m : 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float t = v[c][j] - mc;
+      if (cols % V != 0) t = col + j < cols ? t : 0.0f;
+      if constexpr (V == 8) s1 += t;
+      s2 = __builtin_fmaf(t, t, s2);
     }
   }
-  return s;
+  squares = (double)wave_sum(s2);
+  if constexpr (V == 8) {
+    const double d = (double)wave_sum(s1);
+    mean = __builtin_fma(d, part.inv, (double)m);
+    squares = __builtin_fma(-d * part.inv, d, squares);
+  }
 }
 
 // Rows to their normalised form in place; the reciprocal of the spread.  The
-// squares are of values centred on their wave's mean and are moved to the row's,
-// n_w (mean_w - mean)^2 for each wave, so that one exchange between the waves
-// serves mean and spread.  Quotients are put right by their remainders: a
-// constant row's mean is its value.
+// waves' squares are moved to the row's mean, n_w (mean_w - mean)^2 for each, so
+// that one exchange between the waves serves mean and spread.
 template <typename T, int NC, int W>
 __device__ __forceinline__ float normalise(float (&v)[NC][kVec<T>], int32_t cols, int kind,
-                                           float eta, double (*lds)[2][kThreads<W> / 64],
+                                           float eta, const Share& row, const Share& part, double (*lds)[2][kThreads<W> / 64],
                                            int& half) {
   constexpr int V = kVec<T>;
   const int wave = threadIdx.x >> 6, first = wave & ~(W - 1);
   double squares;
   float mu = 0.0f, off = 0.0f;
   if (kind == kNormLayer) {
-    auto quotient = [](double s, double n) {
-      const double inv = n > 0.0 ? 1.0 / n : 0.0, m = s * inv;
-      return __builtin_fma(__builtin_fma(-m, n, s), inv, m);
-    };
-    const double s = wave_sum(lane_sum<T, NC>(v));
-    double mean = quotient(s, (double)wave_cols<T, NC, W>(wave & (W - 1), cols));
-    mu = (float)mean;
-    float s2 = 0.0f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      // lanes that hold none of the row, and elements past its end, add nothing
-      const int32_t col = chunk_col<T, W>(c);
-      const float m = col < cols ? mu : 0.0f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float t = v[c][j] - m;
-        if (cols % V != 0) t = col + j < cols ? t : 0.0f;
-        s2 = __builtin_fmaf(t, t, s2);
-      }
-    }
-    squares = (double)wave_sum(s2);
+    double mean;
+    wave_moments<T, NC, W>(v, cols, part, mean, squares);
     if constexpr (W > 1) {
       if ((threadIdx.x & 63) == 0) {
-        lds[half][0][wave] = s;
+        lds[half][0][wave] = mean;
         lds[half][1][wave] = squares;
       }
       __syncthreads();
       double all = 0.0;
 #pragma unroll 4
-      for (int i = 0; i < W; ++i) all += lds[half][0][first + i];
-      mean = quotient(all, (double)cols);
+      for (int i = 0; i < W; ++i)
+        all = __builtin_fma((double)wave_cols<T, NC, W>(i, cols), lds[half][0][first + i], all);
+      mean = quotient(all, row.n, row.inv);
       squares = 0.0;
-#pragma unroll 2
+#pragma unroll 4
       for (int i = 0; i < W; ++i) {
         const double n = (double)wave_cols<T, NC, W>(i, cols);
-        const double d = quotient(lds[half][0][first + i], n) - mean;
-        squares += n > 0.0 ? __builtin_fma(n * d, d, lds[half][1][first + i]) : 0.0;
+        const double d = lds[half][0][first + i] - mean;
+        squares += __builtin_fma(n * d, d, lds[half][1][first + i]);
       }
       half ^= 1;
-      mu = (float)mean;
     }
+    mu = (float)mean;
     off = (float)(mean - (double)mu);
   } else {
     float s2 = 0.0f;
@@ -193,7 +223,7 @@ __device__ __forceinline__ float normalise(float (&v)[NC][kVec<T>], int32_t cols
       half ^= 1;
     }
   }
-  const float rs = 1.0f / __builtin_sqrtf((float)(squares / (double)cols) + eta);
+  const float rs = 1.0f / __builtin_sqrtf((float)(squares * row.inv) + eta);
   if (kind == kNormLayer) {
     const float low = -off * rs;
 #pragma unroll
@@ -297,12 +327,13 @@ __device__ __forceinline__ int32_t wave_row() {
 }
 
 template <typename T, int NC, int W>
-__global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_fwd(JoinFwd a) {
+__global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_fwd(JoinFwd args) {
+  JoinFwd a = arguments(args);
   constexpr int V = kVec<T>, R = kRows<W>;
   __shared__ double lds[2][2][kThreads<W> / 64];
   int half = 0;
   const int32_t cols = a.cols, groups = (cols + kAct8Group - 1) / kAct8Group;
-  const int64_t stride = (int64_t)gridDim.x * R;
+  const int64_t rows = a.rows, stride = (int64_t)gridDim.x * R;
   const bool first_lane = (threadIdx.x & (W * 64 - 1)) == 0;
   const RngKey key = load_key(a.drop);
   int64_t r = (int64_t)blockIdx.x * R + wave_row<W>();
@@ -311,17 +342,21 @@ __global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_fwd(JoinFwd a) {
   auto load = [&](const void* from, int64_t ld, int64_t row, lu4 (&to)[NC]) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-      to[c] = load_raw(static_cast<const T*>(from) + row * ld, chunk_col<T, W>(c), cols);
+      to[c] = load_raw(global(static_cast<const T*>(from)) + row * ld, chunk_col<T, W>(c), cols);
   };
   if (A && r < a.rows) {
     load(a.x, a.ldx, r, nx);
     if (a.b) load(a.b, a.ldb, r, nb);
   }
-  const Params<T, NC, W> gate(a.gate, 1.0f, cols), gb(a.gamma_b, 1.0f, cols),
-      bb(a.beta_b, 0.0f, cols), ga(a.gamma, 1.0f, cols), be(a.beta, 0.0f, cols);
+  const Params<T, NC, W> gate(global(a.gate), 1.0f, cols), gb(global(a.gamma_b), 1.0f, cols),
+      bb(global(a.beta_b), 0.0f, cols), ga(global(a.gamma), 1.0f, cols),
+      be(global(a.beta), 0.0f, cols);
+  const Share row = share_of(cols),
+              part = share_of(wave_cols<T, NC, W>((threadIdx.x >> 6) & (W - 1), cols));
   // the rows of a block go round together: its waves meet at the sums' barriers
-  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += stride, r += stride) {
-    const bool in = r < a.rows, more = r + stride < a.rows;
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < rows; r0 += stride, r += stride) {
+    const bool in = r < rows, more = r + stride < rows;
+    a = arguments(args);
     const lu4 none = {0u, 0u, 0u, 0u};
     float v[NC][V];
     if (!A && a.b && in) load(a.b, a.ldb, r, nb);
@@ -331,12 +366,12 @@ __global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_fwd(JoinFwd a) {
     if (A && a.b && more) load(a.b, a.ldb, r + stride, nb);
     if (a.b) {
       if (a.gamma_b) {
-        const float rs = normalise<T, NC, W>(v, cols, a.kind, a.eta, lds, half);
-        if (in && first_lane) a.rstd_b[r] = rs;
+        const float rs = normalise<T, NC, W>(v, cols, a.kind, a.eta, row, part, lds, half);
+        if (in && first_lane) global(a.rstd_b)[r] = rs;
       }
       if (a.qb && in) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) keep<T>(v[c], a.qb, a.eb, r, groups, chunk_col<T, W>(c));
+        for (int c = 0; c < NC; ++c) keep<T>(v[c], global(a.qb), global(a.eb), r, groups, chunk_col<T, W>(c));
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -355,6 +390,7 @@ __global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_fwd(JoinFwd a) {
         }
       }
     }
+    a = arguments(args);
     if (!A && in) load(a.x, a.ldx, r, nx);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -367,22 +403,23 @@ __global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_fwd(JoinFwd a) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
-      if (a.r && in && col < cols) store_row(static_cast<T*>(a.r) + r * a.ldr, col, cols, v[c]);
+      if (a.r && in && col < cols) store_row(global(static_cast<T*>(a.r)) + r * a.ldr, col, cols, v[c]);
     }
+    a = arguments(args);
     if (!a.gamma) continue;
-    const float rs = normalise<T, NC, W>(v, cols, a.kind, a.eta, lds, half);
+    const float rs = normalise<T, NC, W>(v, cols, a.kind, a.eta, row, part, lds, half);
     if (!in) continue;
-    if (first_lane) a.rstd[r] = rs;
+    if (first_lane) global(a.rstd)[r] = rs;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int32_t col = chunk_col<T, W>(c);
-      if (a.q) keep<T>(v[c], a.q, a.e, r, groups, col);
+      if (a.q) keep<T>(v[c], global(a.q), global(a.e), r, groups, col);
       float f[V], o[V];
       ga.get(c, cols, f);
       be.get(c, cols, o);
 #pragma unroll
       for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(v[c][j], f[j], o[j]);
-      if (col < cols) store_row(static_cast<T*>(a.z) + r * a.ldz, col, cols, v[c]);
+      if (col < cols) store_row(global(static_cast<T*>(a.z)) + r * a.ldz, col, cols, v[c]);
     }
   }
 }

@@ -32,7 +32,10 @@ __device__ __forceinline__ RngKey load_key(const Dropout& d) {
   RngKey k{0u, 0u, 0u};
   if (d.threshold) {
     const uint64_t seed = d.rng[0], step = d.rng[1];
-    k = RngKey{(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)step};
+    auto uniform = [](uint64_t v) {
+      return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    };
+    k = RngKey{uniform(seed), uniform(seed >> 32), uniform(step)};
   }
   return k;
 }
@@ -40,6 +43,11 @@ __device__ __forceinline__ RngKey load_key(const Dropout& d) {
 __device__ __forceinline__ lu4 philox(uint64_t block, uint32_t site, const RngKey& key) {
   uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = site, c3 = key.step;
   uint32_t k0 = key.k0, k1 = key.k1;
+#if defined(__HIP_DEVICE_COMPILE__)
+  // each round's key is made where it is used: 20 of them kept over a loop of rows
+  // pushed other scalars out of their registers
+  asm volatile("" : "+s"(k0), "+s"(k1));
+#endif
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
