@@ -17,6 +17,7 @@
 #include "layer.hpp"
 #include "sublayer_kernels.hpp"
 #include "tile.hpp"
+#include "wide.hpp"
 
 namespace oba {
 
@@ -290,6 +291,315 @@ __global__ __launch_bounds__(WA* WB * 64, 3) void k_gated(Gated a, Tiles t) {
   }
 }
 
+// ---- the products of many tiles ------------------------------------------------------
+// Blocks of eight waves, one to a CU, walk tiles of 256 rows by 256 rows of the
+// other operand: forward 128 columns of p and of u, back 256 hidden columns.  A
+// wave holds 64 hidden columns (forward of p and of u) in four tiles of 16 and 64
+// or 128 rows.
+//
+// A step's products are in two halves of 32 along k.  The first half's fragments
+// are in registers when the step begins, the second's are read under the first's
+// products; then all waves meet, the step's half of LDS takes the loads of the step
+// after next, and the next step's first fragments are read under the second half's
+// products.
+//
+// The epilogue works in the registers that the products leave: a lane has four
+// columns of each of four tiles, groups of 32 columns are in four lanes, and a
+// transposition between the four groups of 16 lanes gives each lane 16 columns to
+// store.
+__device__ __forceinline__ int32_t persistent_tile(int32_t round, int32_t tiles) {
+  // each XCD (blocks are handed to the 8 in turn) walks a range of neighbouring
+  // tiles, so that its L2 sees an operand's rows once
+  const int32_t x = blockIdx.x & 7, i = (blockIdx.x >> 3) + round * (int32_t)(gridDim.x >> 3);
+  const int32_t q = tiles / 8, r = tiles % 8, mine = q + (x < r ? 1 : 0);
+  return i < mine ? x * q + min(x, r) + i : -1;
+}
+
+// 16 values of a lane (four of each of four tiles) to 8 bits, 16 bytes a lane;
+// tiles 0 and 1 are one group of 32 columns, 2 and 3 the next.
+__device__ __forceinline__ void keep16(const float (&v)[2][8], bool store, int64_t at_q,
+                                       int64_t at_e, bool store_e, int8_t* q, uint8_t* e) {
+  uint32_t w[4], ex[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t x = group_exp(max_groups(magnitude8(v[h])));
+    const float inv = inv_step_of(x), step = step_of(x);
+    w[2 * h] = quant4(v[h], inv, step, x != 255u);
+    w[2 * h + 1] = quant4(v[h] + 4, inv, step, x != 255u);
+    ex[h] = x;
+  }
+  transpose4(w);
+  if (store) *reinterpret_cast<lu4*>(q + at_q) = lu4{w[0], w[1], w[2], w[3]};
+  // groups of 16 lanes 0 and 2 hold tiles 0 and 2
+  if (store_e) e[at_e] = (uint8_t)((threadIdx.x & 32) ? ex[1] : ex[0]);
+}
+
+// 16 results of a lane to the 16 columns from c that it holds after transposing.
+template <typename T>
+__device__ __forceinline__ void store16(const float (&v)[2][8], bool in_rows, T* row, int32_t c,
+                                        int32_t cols, bool vec) {
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[2 * h + i] = pack2(v[h][4 * i], v[h][4 * i + 1], (const T*)nullptr);
+      b[2 * h + i] = pack2(v[h][4 * i + 2], v[h][4 * i + 3], (const T*)nullptr);
+    }
+  transpose4(a);
+  transpose4(b);
+  if (!in_rows || c >= cols) return;
+  if (vec && c + 16 <= cols) {
+    reinterpret_cast<lu4*>(row + c)[0] = lu4{a[0], b[0], a[1], b[1]};
+    reinterpret_cast<lu4*>(row + c)[1] = lu4{a[2], b[2], a[3], b[3]};
+  } else {
+    uint16_t* p = reinterpret_cast<uint16_t*>(row + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c + 4 * i < cols) p[4 * i] = (uint16_t)a[i];
+      if (c + 4 * i + 1 < cols) p[4 * i + 1] = (uint16_t)(a[i] >> 16);
+      if (c + 4 * i + 2 < cols) p[4 * i + 2] = (uint16_t)b[i];
+      if (c + 4 * i + 3 < cols) p[4 * i + 3] = (uint16_t)(b[i] >> 16);
+    }
+  }
+}
+
+template <typename T, GatedKind KIND>
+__global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tiles t) {
+  constexpr bool FWD = KIND == GatedKind::kForward;
+  constexpr int ASRC = FWD ? kKRow : kKCol;
+  constexpr int HC = FWD ? kWideTile / 2 : kWideTile;  // hidden columns of a tile
+  constexpr int WA = HC / 64, WB = 8 / WA;             // waves along the columns and the rows
+  constexpr int TA = FWD ? 8 : 4, TB = kWideTile / 16 / WB;
+  __shared__ __align__(1024) char lds[2 * kWideStep];
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wa = wave % WA, wb = wave / WA;
+  const int32_t tiles = t.ta * t.tb;
+  const int32_t full = (int32_t)(args.k / kBK), rest = (int32_t)(args.k % kBK);
+  const int32_t steps = full + (rest > 0);
+
+  WideStage<ASRC, HC> sa;
+  WideStage<kKRow, kWideTile> sb;
+  const char *ap, *ap2, *bp;
+  int64_t astep;
+  int32_t r0, c0;
+  // the operands of a tile
+  auto begin = [&](int32_t tile) __attribute__((always_inline)) {
+    const Gated a = arguments(args);
+    // four rows of tiles together, along the columns: the tiles that run at one
+    // time share operands of both sides
+    const int32_t super = tile / (4 * t.ta), in = tile - super * 4 * t.ta;
+    const int32_t high = min(4, t.tb - super * 4);
+    r0 = (super * 4 + in % high) * kWideTile;
+    c0 = in / high * HC;
+    if constexpr (FWD) {
+      ap = static_cast<const char*>(a.a) + (int64_t)c0 * a.lda * 2;
+      ap2 = ap + (int64_t)a.cols * a.lda * 2;
+      astep = kBK * 2;
+    } else {
+      ap = ap2 = static_cast<const char*>(a.a) + (int64_t)c0 * 2;
+      astep = kBK * a.lda * 2;
+    }
+    bp = static_cast<const char*>(a.b) + (int64_t)r0 * a.ldb * 2;
+    const uint32_t tid = thread_anew();
+    sa.init(tid, c0, a.cols, (uint32_t)a.lda);
+    sb.init(tid, r0, (int32_t)min(a.rows, (int64_t)0x7FFFFFFF), (uint32_t)a.ldb);
+  };
+  // the loads of step s to its half of LDS.  A sum whose length is no multiple of
+  // the step begins with what is left over, through registers.
+  auto issue = [&](int32_t s) __attribute__((always_inline)) {
+    char* to = lds + (s & 1) * kWideStep;
+    sa.ahead(ap, to);
+    if constexpr (FWD) sa.ahead(ap2, to + kWideHalf / 2);
+    sb.ahead(bp, to + kWideHalf);
+    ap += astep;
+    if constexpr (FWD) ap2 += astep;
+    bp += kBK * 2;
+  };
+  auto issue_first = [&]() __attribute__((always_inline)) {
+    if (rest > 0) {
+      const uint32_t tid = thread_anew();
+      sa.tail(tid, ap + full * astep, lds, rest);
+      if constexpr (FWD) sa.tail(tid, ap2 + full * astep, lds + kWideHalf / 2, rest);
+      sb.tail(tid, bp + (int64_t)full * kBK * 2, lds + kWideHalf, rest);
+    } else {
+      issue(0);
+    }
+    if (steps > 1) issue(1);
+  };
+  Frags<ASRC> ga;
+  Frags<kKRow> gb;
+  ga.init(wa * 64);
+  gb.init(wb * TB * 16);
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(3))) char* lp;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lp)lds;
+#else
+  const uint32_t lds0 = 0;
+#endif
+  auto fragments = [&](int32_t s, int ks, lu4 (&fa)[TA], lu4 (&fb)[TB])
+                       __attribute__((always_inline)) {
+    const uint32_t at = lds0 + (s & 1) * (uint32_t)kWideStep;
+    if constexpr (FWD) {  // the first four of a wave's tiles are p's, the others u's
+      ga.read(at, ks, fa, 0, 4);
+      ga.read(at + kWideHalf / 2, ks, fa, 4, 4);
+    } else {
+      ga.read(at, ks, fa);
+    }
+    gb.read(at + kWideHalf, ks, fb);
+  };
+  lf4 acc[TA][TB];
+  auto products = [&](const lu4 (&fa)[TA], const lu4 (&fb)[TB]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+#pragma unroll
+      for (int i = 0; i < TA; ++i) acc[i][j] = mfma(fa[i], fb[j], acc[i][j], (const T*)nullptr);
+  };
+
+  int32_t round = 0, tile = persistent_tile(0, tiles);
+  if (tile < 0) return;
+  begin(tile);
+  issue_first();
+  wait_loads();
+  meet();
+  while (true) {
+    const int32_t rt = r0, cw = c0 + wa * 64;  // the wave's first column
+    {
+      const Gated a = arguments(args);
+      const int32_t lg = (thread_anew() & 63) >> 4;
+#pragma unroll
+      for (int i = 0; i < TA; ++i) {
+        lf4 first = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (FWD) {
+          if (a.bias) {
+            const float* b = global(a.bias) + (i < 4 ? 0 : a.cols);
+            for (int m = 0; m < 4; ++m)
+              first[m] = b[min(cw + i % 4 * 16 + lg * 4 + m, a.cols - 1)];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < TB; ++j) acc[i][j] = first;
+      }
+    }
+    lu4 fa0[TA], fb0[TB], fa1[TA], fb1[TB];
+    fragments(0, 0, fa0, fb0);
+    const int32_t next = persistent_tile(round + 1, tiles);
+#pragma unroll 1
+    for (int32_t s = 0; s < steps; ++s) {
+      fragments(s, 1, fa1, fb1);
+      products(fa0, fb0);
+      if (s > 0) wait_loads();  // those of step s + 1
+      meet();                   // every wave has read all of step s
+      if (s + 2 < steps) issue(s + 2);
+      if (s + 1 < steps) fragments(s + 1, 0, fa0, fb0);
+      products(fa1, fb1);
+    }
+    // LDS is free: the next tile's first steps
+    if (next >= 0) {
+      begin(next);
+      issue_first();
+    }
+
+    // ---- the tile's results ----
+    const Gated a = arguments(args);
+    const uint32_t tid = thread_anew();
+    const int32_t l = tid & 63, lg = l >> 4;
+    const int64_t groups = groups_of(a.cols);
+    const int32_t cl = cw + lg * 16;  // the lane's columns after transposing
+    const bool edge = cw + 64 > a.cols;
+    const bool vec = FWD || a.cols % 8 == 0;
+    // kept pre-activations of the row's 16 columns, a row of tiles ahead
+    lu4 kp, ku;
+    uint32_t ep[2], eu[2];
+    auto load_pre = [&](int j) __attribute__((always_inline)) {
+      const int64_t r = min((int64_t)rt + (wb * TB + j) * 16 + (l & 15), a.rows - 1);
+      const int64_t g = r * groups + min(cl / kAct8Group, (int32_t)groups - 1);
+      const int64_t at = g * kAct8Group + (cl & 16);
+      kp = *reinterpret_cast<const lu4*>(global(a.qp) + at);
+      ku = *reinterpret_cast<const lu4*>(global(a.qu) + at);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t gg = r * groups + min(cw / kAct8Group + h, (int32_t)groups - 1);
+        ep[h] = global(a.ep)[gg];
+        eu[h] = global(a.eu)[gg];
+      }
+    };
+    if constexpr (!FWD) load_pre(0);
+#pragma unroll 1
+    for (int j = 0; j < TB; ++j) {
+      const int64_t r = (int64_t)rt + (wb * TB + j) * 16 + (l & 15);
+      const bool in_rows = r < a.rows;
+      // the accumulators of this j, by constant indexes
+      float x[TA / 2][8];
+#pragma unroll
+      for (int jj = 0; jj < TB; ++jj) {
+        if (jj > 0 && jj != j) continue;
+#pragma unroll
+        for (int i = 0; i < TA; ++i)
+          for (int m = 0; m < 4; ++m) x[i / 2][i % 2 * 4 + m] = acc[i][jj][m];
+      }
+      T* row = global(static_cast<T*>(a.c)) + r * a.ldc;
+      if constexpr (FWD) {
+        if (edge) {  // columns past the last are kept as 0
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            for (int m = 0; m < 4; ++m)
+              if (cw + i % 4 * 16 + lg * 4 + m >= a.cols) x[i / 2][i % 2 * 4 + m] = 0.0f;
+        }
+        float (&p)[2][8] = reinterpret_cast<float (&)[2][8]>(x[0]);
+        float (&u)[2][8] = reinterpret_cast<float (&)[2][8]>(x[2]);
+        const int64_t at_e = r * groups + cl / kAct8Group;
+        const int64_t at_q = at_e * kAct8Group + (cl & 16);
+        const bool in = in_rows && cl / kAct8Group < groups, in_e = in && (lg & 1) == 0;
+        if (j == 0) wait_loads();  // the next tile's steps, before stores that would be waited for
+        if (a.qp) {
+          keep16(p, in, at_q, at_e, in_e, global(a.qp), global(a.ep));
+          keep16(u, in, at_q, at_e, in_e, global(a.qu), global(a.eu));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          gate_value(p[h], a.gate);
+          for (int m = 0; m < 8; ++m) p[h][m] *= u[h][m];
+        }
+        if (a.q) {  // as rounded: what reading y and encoding it would give
+          float y[2][8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) unpack(pack(p[h], (const T*)nullptr), y[h], (const T*)nullptr);
+          keep16(y, in, at_q, at_e, in_e, global(a.q), global(a.e));
+        }
+        store16<T>(p, in_rows, row, cl, a.cols, vec);
+      } else {
+        float (&d)[2][8] = reinterpret_cast<float (&)[2][8]>(x[0]);
+        uint32_t wp[4] = {kp[0], kp[1], kp[2], kp[3]}, wu[4] = {ku[0], ku[1], ku[2], ku[3]};
+        const float sp[2] = {step_of(ep[0]), step_of(ep[1])};
+        const float su[2] = {step_of(eu[0]), step_of(eu[1])};
+        if (j + 1 < TB) load_pre(j + 1);
+        if (j == 0) wait_loads();
+        transpose4(wp);
+        transpose4(wu);
+        float f[2][8], df[2][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int m = 0; m < 8; ++m) f[h][m] = dequant(wp[2 * h + m / 4], m % 4, sp[h]);
+          gate_both(f[h], df[h], a.gate);
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            df[h][m] *= d[h][m] * dequant(wu[2 * h + m / 4], m % 4, su[h]);
+            f[h][m] *= d[h][m];
+          }
+        }
+        store16<T>(df, in_rows, row, cl, a.cols, true);
+        store16<T>(f, in_rows, row + a.cols, cl, a.cols, vec);
+      }
+    }
+    if (next < 0) break;
+    ++round;
+    meet();  // every wave's loads of the next tile have landed
+  }
+}
+
 // ---- joining a split product ------------------------------------------------------
 // A thread adds eight columns' sums in split order and finishes them as above;
 // four lanes hold a group of 32 columns.
@@ -356,8 +666,21 @@ Tiles choose(GatedKind kind, int64_t rows, int32_t cols, int64_t k) {
   return t;
 }
 
+// Whether the tiles of 256 x 256 give every CU work.
+bool wide(GatedKind kind, int64_t rows, int32_t cols) {
+  const int64_t c = kind == GatedKind::kForward ? kWideTile / 2 : kWideTile;
+  return (cols + c - 1) / c * ((rows + kWideTile - 1) / kWideTile) >= kCUs / 2;
+}
+
 template <typename T, GatedKind KIND>
 void product(const Gated& a, hipStream_t st) {
+  if (wide(KIND, a.rows, a.cols)) {
+    constexpr int32_t c = KIND == GatedKind::kForward ? kWideTile / 2 : kWideTile;
+    const Tiles t{(a.cols + c - 1) / c, (int32_t)((a.rows + kWideTile - 1) / kWideTile), 1, 0};
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gated_wide<T, KIND>), dim3(kCUs), dim3(kWideThreads), 0,
+                       st, a, t);
+    return;
+  }
   const Tiles t = choose(KIND, a.rows, a.cols, a.k);
   const uint32_t grid = (uint32_t)gated_blocks(KIND, a.rows, a.cols, a.k);
   hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gated<T, KIND, kTile, kTile, 2, 2>), dim3(grid), dim3(256),

@@ -36,27 +36,6 @@ namespace oba {
 
 namespace {
 
-// A pointer that came out of memory, as one to global memory.
-template <typename P>
-__device__ __forceinline__ P* global(P* p) {
-  return (P*)(__attribute__((address_space(1))) P*)p;
-}
-
-// The kernel's argument block, read again where it is asked for: its 30 pointers
-// and strides do not fit the scalar registers together, and kept for all of a
-// kernel they spilled (46 scalar registers, and vector registers to hold them).
-template <typename A>
-__device__ __forceinline__ A arguments(const A& a) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  typedef const __attribute__((address_space(4))) A* Block;
-  Block p = (Block)__builtin_amdgcn_kernarg_segment_ptr();
-  asm volatile("" : "+s"(p));
-  return *p;
-#else
-  return a;
-#endif
-}
-
 // W waves to a row; blocks of 8 waves hold 8 / W rows at a time, 16 waves one.
 template <int W>
 constexpr int kThreads = W == 16 ? 1024 : 512;

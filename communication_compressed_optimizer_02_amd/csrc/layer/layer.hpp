@@ -26,6 +26,28 @@ typedef float lf4 __attribute__((ext_vector_type(4)));
 typedef uint32_t lu2 __attribute__((ext_vector_type(2)));
 typedef uint32_t lu4 __attribute__((ext_vector_type(4)));
 
+// A pointer that came out of memory, as one to global memory.
+template <typename P>
+__device__ __forceinline__ P* global(P* p) {
+  return (P*)(__attribute__((address_space(1))) P*)p;
+}
+
+// A kernel's first argument, a block of pointers and sizes, read again where it is
+// asked for.  The larger blocks do not fit the scalar registers together with the
+// rest: kept for all of a kernel they spilled (46 scalar registers in the join's
+// backward pass, 94 in the gated product's), and vector registers to hold them.
+template <typename A>
+__device__ __forceinline__ A arguments(const A& a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef const __attribute__((address_space(4))) A* Block;
+  Block p = (Block)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *p;
+#else
+  return a;
+#endif
+}
+
 // Elements of a row that one lane holds: 16 bytes.
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);

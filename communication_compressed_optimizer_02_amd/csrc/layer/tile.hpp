@@ -15,6 +15,7 @@
 #include <cstdint>
 
 #include "layer.hpp"
+#include "layer_kernels.hpp"
 
 namespace oba {
 

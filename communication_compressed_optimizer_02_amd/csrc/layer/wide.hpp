@@ -1,0 +1,206 @@
+// wide.hpp -- a 256 x 256 tile of a product by eight waves, for results of many
+// tiles (gated.hip): the loads of a step in flight under the products of the step
+// before, and the results taken from the accumulators without LDS, so that the
+// next tile's first steps are loaded under this one's epilogue.
+//
+// Operands and their layouts in LDS are those of tile.hpp: a step of 64 along k is
+// 64 KB, two of them fill 128 of the CU's 160 KB.  The direct loads to LDS are
+// written in assembly: of the builtin's the compiler waits for all before the next
+// read of LDS, also where that read is of the other half.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "layer.hpp"
+#include "tile.hpp"
+
+namespace oba {
+
+namespace {
+
+constexpr int kWideThreads = 512;
+constexpr int kWideTile = 256;
+constexpr int kWideHalf = kWideTile * kBK * 2;   // bytes of one operand's step
+constexpr int kWideStep = 2 * kWideHalf;
+
+// The thread's number, which the compiler takes for a new one: what is worked out
+// from it for one phase of a tile is not kept in registers through the others.
+__device__ __forceinline__ uint32_t thread_anew() {
+  uint32_t t = threadIdx.x;
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(t));
+#endif
+  return t;
+}
+
+// One thread's share of an operand of R rows, as Stage's of tile.hpp.
+template <int SRC, int R>
+struct WideStage {
+  static constexpr int P = R * (kBK / 8) / kWideThreads;
+  uint32_t off[P];  // bytes from the step's origin
+
+  __device__ __forceinline__ static uint32_t k_of(uint32_t i) {
+    return SRC == kKRow ? ((i % (kBK / 8)) ^ (i / (kBK / 8) & 7u)) * 8 : i / (R / 8);
+  }
+  // r0: first row of the tile, of `rows`; rows past the last read the last
+  __device__ __forceinline__ void init(uint32_t tid, int32_t r0, int32_t rows, uint32_t ld) {
+    const uint32_t last = (uint32_t)(rows - 1 - r0);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const uint32_t i = p * kWideThreads + tid, k = k_of(i);
+      if constexpr (SRC == kKRow) {
+        off[p] = (min(i / (kBK / 8), last) * ld + k) * 2;
+      } else {
+        const uint32_t c = i % (R / 8), block = kcol_block<R>(k, c / 2);
+        off[p] = (k * ld + min(block * 16 + (c & 1) * 8, last & ~7u)) * 2;
+      }
+    }
+  }
+
+  // A whole step straight to LDS, without a wait.  Five wait states lie between a
+  // vector instruction's write of a scalar register (the buffer's) and a load that
+  // reads it, one between the write of m0 and the load; nothing else in these
+  // kernels uses m0.
+  __device__ __forceinline__ void ahead(const char* base, char* lds) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef __attribute__((address_space(3))) char* lp;
+    typedef int i4 __attribute__((ext_vector_type(4)));
+    const uint64_t b = (uint64_t)base;
+    const i4 r = {(int)__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+                  (int)__builtin_amdgcn_readfirstlane((int)((uint32_t)(b >> 32) & 0xFFFFu)), -1,
+                  0x00027000};
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t to = (uint32_t)(uintptr_t)(lp)lds + wave * 1024u;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                   :
+                   : "s"(to + p * kWideThreads * 16), "v"(off[p]), "s"(r)
+                   : "memory");
+#endif
+  }
+
+  // A step of fewer than kBK elements through registers, 0 past them.
+  __device__ __forceinline__ void tail(uint32_t tid, const char* base, char* lds,
+                                       int32_t left) const {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int32_t k = (int32_t)k_of(p * kWideThreads + tid);
+      lu4 u = {0u, 0u, 0u, 0u};
+      if (k < left) {
+        u = *reinterpret_cast<const lu4*>(global(base) + off[p]);
+        if (SRC == kKRow && k + 8 > left) {
+          for (int j = 0; j < 4; ++j)
+            u[j] &= (k + 2 * j < left ? 0xFFFFu : 0u) | (k + 2 * j + 1 < left ? 0xFFFF0000u : 0u);
+        }
+      }
+      *reinterpret_cast<lu4*>(lds + (p * kWideThreads + tid) * 16) = u;
+    }
+  }
+};
+
+// Where a wave's fragments lie in a step's operand, worked out once: the layouts of
+// tile.hpp for rows row0 .. row0 + 16 n - 1, row0 a multiple of 64.  What is left
+// of an address from fragment to fragment is a constant (kKRow) or one of four
+// (kKCol, four fragments).
+template <int SRC>
+struct Frags;
+
+template <>
+struct Frags<kKRow> {
+  uint32_t at[2];  // of the two halves along k
+  __device__ __forceinline__ void init(uint32_t row0) {
+    const uint32_t l = threadIdx.x & 63, r = l & 15;
+    at[0] = (row0 + r) * 128u + (((l >> 4) ^ (r & 7u)) << 4);
+    at[1] = at[0] ^ 64u;
+  }
+  template <int N>
+  __device__ __forceinline__ void read(uint32_t lds, int ks, lu4 (&f)[N], int first = 0,
+                                       int n = N) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef const __attribute__((address_space(3))) lu4* lp;
+    const uint32_t b = lds + at[ks];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i >= first && i < first + n) f[i] = *(lp)(b + (i - first) * 2048u);
+#endif
+  }
+};
+
+template <>
+struct Frags<kKCol> {
+  uint32_t at[4];
+  __device__ __forceinline__ void init(uint32_t row0) {
+    const uint32_t l = threadIdx.x & 63, k = (l >> 4) * 8 + ((l & 15) >> 2);
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+      at[i] = kcol_at<kWideTile>(k, (row0 >> 4) + i) + (l & 3) * 8;
+  }
+  __device__ __forceinline__ void read(uint32_t lds, int ks, lu4 (&f)[4]) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef __attribute__((address_space(3))) s4* lp;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = lds + at[i] + ks * (32 * kWideTile * 2);
+      const lu2 lo = __builtin_bit_cast(lu2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)b));
+      const lu2 hi = __builtin_bit_cast(
+          lu2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(b + 4 * kWideTile * 2)));
+      f[i] = lu4{lo[0], lo[1], hi[0], hi[1]};
+    }
+#endif
+  }
+};
+
+// Every load to LDS of this wave has landed.
+__device__ __forceinline__ void wait_loads() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#endif
+}
+// Every read of LDS of this wave has returned; all waves meet.
+__device__ __forceinline__ void meet() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+// ---- across the four groups of 16 lanes ------------------------------------------
+// Lane group g holds row l % 16's columns 4 g .. 4 g + 3 of a 16 x 16 tile.
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+#endif
+}
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+#endif
+}
+// The largest of the four groups' values, in all of them.
+__device__ __forceinline__ uint32_t max_groups(uint32_t v) {
+  uint32_t w = v;
+  swap16(v, w);
+  v = w = max(v, w);
+  swap32(v, w);
+  return max(v, w);
+}
+// Transposes words of four tiles: before, group g holds word g of tiles 0 .. 3,
+// after it words 0 .. 3 of tile g.  It is its own inverse.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+  swap16(w[0], w[1]);
+  swap16(w[2], w[3]);
+  swap32(w[0], w[2]);
+  swap32(w[1], w[3]);
+}
+
+}  // namespace
+}  // namespace oba

@@ -15,7 +15,10 @@ TWO = ("f16", "bf16")
 # rows, in, hidden (forward); rows, out, hidden (gradient)
 SHAPES = [(1, 1, 1), (1, 40, 72), (1, 1600, 6400), (3, 64, 64), (7, 33, 129), (16, 5000, 16),
           (33, 520, 200), (64, 4096, 100), (130, 200, 77), (128, 128, 128), (257, 72, 400),
-          (515, 777, 1001), (2000, 1000, 24), (1500, 40, 3600), (700, 1100, 513)]
+          (515, 777, 1001), (2000, 1000, 24), (1500, 40, 3600), (700, 1100, 513),
+          # results of many tiles: more tiles than CUs, sums of one step, of a part of
+          # one, of whole steps and of a remainder
+          (8200, 40, 1033), (4100, 64, 2050), (8193, 128, 1040), (2300, 777, 4000)]
 
 
 def say(*a):
