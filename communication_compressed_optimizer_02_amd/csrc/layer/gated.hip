@@ -12,6 +12,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "gate.hpp"
 #include "layer.hpp"
@@ -299,9 +300,8 @@ __global__ __launch_bounds__(WA* WB * 64, 3) void k_gated(Gated a, Tiles t) {
 //
 // A step's products are in two halves of 32 along k.  The first half's fragments
 // are in registers when the step begins, the second's are read under the first's
-// products; then all waves meet, the step's half of LDS takes the loads of the step
-// after next, and the next step's first fragments are read under the second half's
-// products.
+// products; then all waves meet, the step's parts of LDS take loads of later steps,
+// and the next step's first fragments are read under the second half's products.
 //
 // The epilogue works in the registers that the products leave: a lane has four
 // columns of each of four tiles, groups of 32 columns are in four lanes, and a
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
   constexpr int HC = FWD ? kWideTile / 2 : kWideTile;  // hidden columns of a tile
   constexpr int WA = HC / 64, WB = 8 / WA;             // waves along the columns and the rows
   constexpr int TA = FWD ? 8 : 4, TB = kWideTile / 16 / WB;
-  __shared__ __align__(1024) char lds[2 * kWideStep];
+  __shared__ __align__(1024) char lds[kWideLds];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wa = wave % WA, wb = wave / WA;
@@ -381,10 +381,11 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
 
   WideStage<ASRC, HC> sa;
   WideStage<kKRow, kWideTile> sb;
-  const char *ap, *ap2, *bp;
+  const char *ap, *ap2, *bp;  // of the step to be loaded next
+  const char *rest_a, *rest_b;
   int64_t astep;
   int32_t r0, c0;
-  // the operands of a tile
+  // the operands of the tile to be loaded next
   auto begin = [&](int32_t tile) __attribute__((always_inline)) {
     const Gated a = arguments(args);
     // four rows of tiles together, along the columns: the tiles that run at one
@@ -402,31 +403,34 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
       astep = kBK * a.lda * 2;
     }
     bp = static_cast<const char*>(a.b) + (int64_t)r0 * a.ldb * 2;
+    rest_a = ap + full * astep;
+    rest_b = bp + (int64_t)full * kBK * 2;
     const uint32_t tid = thread_anew();
     sa.init(tid, c0, a.cols, (uint32_t)a.lda);
     sb.init(tid, r0, (int32_t)min(a.rows, (int64_t)0x7FFFFFFF), (uint32_t)a.ldb);
   };
-  // the loads of step s to its half of LDS.  A sum whose length is no multiple of
-  // the step begins with what is left over, through registers.
-  auto issue = [&](int32_t s) __attribute__((always_inline)) {
-    char* to = lds + (s & 1) * kWideStep;
-    sa.ahead(ap, to);
-    if constexpr (FWD) sa.ahead(ap2, to + kWideHalf / 2);
-    sb.ahead(bp, to + kWideHalf);
-    ap += astep;
-    if constexpr (FWD) ap2 += astep;
-    bp += kBK * 2;
-  };
-  auto issue_first = [&]() __attribute__((always_inline)) {
-    if (rest > 0) {
-      const uint32_t tid = thread_anew();
-      sa.tail(tid, ap + full * astep, lds, rest);
-      if constexpr (FWD) sa.tail(tid, ap2 + full * astep, lds + kWideHalf / 2, rest);
-      sb.tail(tid, bp + (int64_t)full * kBK * 2, lds + kWideHalf, rest);
-    } else {
-      issue(0);
+  // the next step's loads to a part of LDS, operand by operand, a piece of each
+  // thread's four at a time
+  auto issue_a = [&](int32_t slot, bool to_next, int p) __attribute__((always_inline)) {
+    char* to = lds + slot;
+    if constexpr (FWD) sa.ahead(wave, p < 2 ? ap : ap2, to + (p < 2 ? 0 : kWideHalf / 2), p & 1, 1);
+    else sa.ahead(wave, ap, to, p, 1);
+    if (p == 3) {
+      ap += to_next ? astep : 0;
+      if constexpr (FWD) ap2 += to_next ? astep : 0;
     }
-    if (steps > 1) issue(1);
+  };
+  auto issue_b = [&](int32_t slot, bool to_next, int p) __attribute__((always_inline)) {
+    sb.ahead(wave, bp, lds + kWideA + slot, p, 1);
+    if (p == 3) bp += to_next ? kBK * 2 : 0;
+  };
+  // A sum whose length is no multiple of the step begins with what is left over: its
+  // elements, 0 past them, go over what step 0 loaded there (the first whole step).
+  auto put_rest = [&](int32_t slot_a, int32_t slot_b) __attribute__((always_inline)) {
+    const uint32_t tid = thread_anew();
+    sa.tail(tid, rest_a, lds + slot_a, rest);
+    if constexpr (FWD) sa.tail(tid, rest_a + (ap2 - ap), lds + slot_a + kWideHalf / 2, rest);
+    sb.tail(tid, rest_b, lds + kWideA + slot_b, rest);
   };
   Frags<ASRC> ga;
   Frags<kKRow> gb;
@@ -438,31 +442,56 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
 #else
   const uint32_t lds0 = 0;
 #endif
-  auto fragments = [&](int32_t s, int ks, lu4 (&fa)[TA], lu4 (&fb)[TB])
-                       __attribute__((always_inline)) {
-    const uint32_t at = lds0 + (s & 1) * (uint32_t)kWideStep;
-    if constexpr (FWD) {  // the first four of a wave's tiles are p's, the others u's
-      ga.read(at, ks, fa, 0, 4);
-      ga.read(at + kWideHalf / 2, ks, fa, 4, 4);
+  // Of half a step's fragments the four of one operand are used throughout, the
+  // eight of the other four products long each: read in this order, behind these
+  // products of the half before, a fragment takes the registers of one that is done.
+  constexpr bool kAlong = TA > TB;  // whether the first operand has the eight
+  auto read_behind = [&](int m, int32_t slot_a, int32_t slot_b, int ks, lu4 (&fa)[TA],
+                         lu4 (&fb)[TB]) __attribute__((always_inline)) {
+    const int n = m < 4 ? m : m % 4 == 0 ? 3 + m / 4 : m == 30 ? 11 : -1;
+    if (n < 0) return;
+    const bool first = (n < 4) != kAlong;  // whether it is one of the first operand's
+    const int i = n < 4 ? n : n - 4;
+    if (!first) {
+      fb[i % TB] = gb.read(lds0 + kWideA + (uint32_t)slot_b, ks, i);
+    } else if constexpr (FWD) {  // the first four of a wave's tiles are p's, the others u's
+      fa[i % TA] = ga.read(lds0 + (uint32_t)slot_a + (i < 4 ? 0 : kWideHalf / 2), ks, i % 4);
     } else {
-      ga.read(at, ks, fa);
+      fa[i % TA] = ga.read(lds0 + (uint32_t)slot_a, ks, i);
     }
-    gb.read(at + kWideHalf, ks, fb);
   };
+  // The products of half a step, with a piece of other work behind each: a wave
+  // issues in order, and what it issues between products that could follow each
+  // other at once leaves the matrix cores idle.
   lf4 acc[TA][TB];
-  auto products = [&](const lu4 (&fa)[TA], const lu4 (&fb)[TB]) __attribute__((always_inline)) {
+  auto products = [&](const lu4 (&fa)[TA], const lu4 (&fb)[TB], auto&& behind)
+                      __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < TB; ++j)
-#pragma unroll
-      for (int i = 0; i < TA; ++i) acc[i][j] = mfma(fa[i], fb[j], acc[i][j], (const T*)nullptr);
+    for (int m = 0; m < TA * TB; ++m) {
+      const int i = kAlong ? m / 4 : m % 4, j = kAlong ? m % 4 : m / 4;
+      acc[i][j] = mfma(fa[i], fb[j], acc[i][j], (const T*)nullptr);
+      behind(m);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
-
+  auto after = [](int32_t slot) { return slot == 2 * kWideHalf ? 0 : slot + kWideHalf; };
   int32_t round = 0, tile = persistent_tile(0, tiles);
   if (tile < 0) return;
   begin(tile);
-  issue_first();
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) issue_a(s * kWideHalf, s > 0 || rest == 0, p);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) issue_b(s * kWideHalf, s > 0 || rest == 0, p);
+  }
   wait_loads();
+  if (rest > 0) put_rest(0, 0);
   meet();
+  // Step s of a tile lies in a ring of three parts and one of two; its loads are
+  // issued under step s - 2, a tile's first two under the last two of the tile
+  // before (after the last tile once more its own).
+  int32_t slot_a = 0, slot_b = 0;
   while (true) {
     const int32_t rt = r0, cw = c0 + wa * 64;  // the wave's first column
     {
@@ -483,22 +512,32 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
       }
     }
     lu4 fa0[TA], fb0[TB], fa1[TA], fb1[TB];
-    fragments(0, 0, fa0, fb0);
+#pragma unroll
+    for (int m = 0; m < 32; ++m) read_behind(m, slot_a, slot_b, 0, fa0, fb0);
     const int32_t next = persistent_tile(round + 1, tiles);
 #pragma unroll 1
     for (int32_t s = 0; s < steps; ++s) {
-      fragments(s, 1, fa1, fb1);
-      products(fa0, fb0);
-      if (s > 0) wait_loads();  // those of step s + 1
-      meet();                   // every wave has read all of step s
-      if (s + 2 < steps) issue(s + 2);
-      if (s + 1 < steps) fragments(s + 1, 0, fa0, fb0);
-      products(fa1, fb1);
-    }
-    // LDS is free: the next tile's first steps
-    if (next >= 0) {
-      begin(next);
-      issue_first();
+      if (s == steps - 2) begin(next >= 0 ? next : tile);
+      const bool to_next = rest == 0 || s != steps - 2;
+      const int32_t a1 = after(slot_a), a2 = after(a1), b1 = slot_b ^ kWideHalf;
+      // the first half's products over the reads of the second's fragments and the
+      // loads of the first operand's step s + 2
+      products(fa0, fb0, [&](int m) __attribute__((always_inline)) {
+        read_behind(m, slot_a, slot_b, 1, fa1, fb1);
+        if (m % 8 == 5) issue_a(a2, to_next, m / 8);
+      });
+      // step s + 1 has landed: the second operand's loads of it are the last before
+      // those of the first operand's step s + 2
+      if (s > 0) wait_loads<4>();
+      meet();  // every wave has read all of step s
+      // the second half's over the next step's first fragments and the loads of the
+      // second operand's step s + 2
+      products(fa1, fb1, [&](int m) __attribute__((always_inline)) {
+        read_behind(m, a1, b1, 0, fa0, fb0);
+        if (m % 8 == 5) issue_b(slot_b, to_next, m / 8);
+      });
+      slot_a = a1;
+      slot_b = b1;
     }
 
     // ---- the tile's results ----
@@ -595,8 +634,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
       }
     }
     if (next < 0) break;
+    tile = next;
     ++round;
-    meet();  // every wave's loads of the next tile have landed
+    if (rest > 0) put_rest(slot_a, slot_b);
+    meet();  // every wave's part of the next tile's first steps is there
   }
 }
 
@@ -666,15 +707,17 @@ Tiles choose(GatedKind kind, int64_t rows, int32_t cols, int64_t k) {
   return t;
 }
 
-// Whether the tiles of 256 x 256 give every CU work.
-bool wide(GatedKind kind, int64_t rows, int32_t cols) {
+// Whether the tiles of 256 x 256 give every CU work, and sums have the two whole
+// steps that are loaded ahead.
+bool wide(GatedKind kind, int64_t rows, int32_t cols, int64_t k) {
+  if (k < 2 * kBK) return false;
   const int64_t c = kind == GatedKind::kForward ? kWideTile / 2 : kWideTile;
   return (cols + c - 1) / c * ((rows + kWideTile - 1) / kWideTile) >= kCUs / 2;
 }
 
 template <typename T, GatedKind KIND>
 void product(const Gated& a, hipStream_t st) {
-  if (wide(KIND, a.rows, a.cols)) {
+  if (wide(KIND, a.rows, a.cols, a.k)) {
     constexpr int32_t c = KIND == GatedKind::kForward ? kWideTile / 2 : kWideTile;
     const Tiles t{(a.cols + c - 1) / c, (int32_t)((a.rows + kWideTile - 1) / kWideTile), 1, 0};
     hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gated_wide<T, KIND>), dim3(kCUs), dim3(kWideThreads), 0,

@@ -1,12 +1,15 @@
 // wide.hpp -- a 256 x 256 tile of a product by eight waves, for results of many
-// tiles (gated.hip): the loads of a step in flight under the products of the step
-// before, and the results taken from the accumulators without LDS, so that the
-// next tile's first steps are loaded under this one's epilogue.
+// tiles (gated.hip): loads one and two steps ahead of the products, and the results
+// taken from the accumulators without LDS, so that the next tile's first steps are
+// loaded under this one's epilogue.
 //
 // Operands and their layouts in LDS are those of tile.hpp: a step of 64 along k is
-// 64 KB, two of them fill 128 of the CU's 160 KB.  The direct loads to LDS are
-// written in assembly: of the builtin's the compiler waits for all before the next
-// read of LDS, also where that read is of the other half.
+// 32 KB of each operand.  All 160 KB of the CU's LDS hold three steps of the one
+// operand and two of the other: a CU takes 64 KB in no less than a thousand cycles,
+// which with the latency is as long as a step's products (2048 cycles), so that a
+// step's loads do not all come in under the step before.  The direct loads to LDS
+// are written in assembly: of the builtin's the compiler waits for all before the
+// next read of LDS, also where that read is of another part.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -22,17 +25,20 @@ namespace {
 constexpr int kWideThreads = 512;
 constexpr int kWideTile = 256;
 constexpr int kWideHalf = kWideTile * kBK * 2;   // bytes of one operand's step
-constexpr int kWideStep = 2 * kWideHalf;
+constexpr int kWideA = 3 * kWideHalf;             // the first operand's ring, then the second's
+constexpr int kWideLds = kWideA + 2 * kWideHalf;
 
-// The thread's number, which the compiler takes for a new one: what is worked out
-// from it for one phase of a tile is not kept in registers through the others.
-__device__ __forceinline__ uint32_t thread_anew() {
-  uint32_t t = threadIdx.x;
+// A value that the compiler takes for a new one: what follows from it is worked out
+// where it is used, and not kept in registers that the products need.
+__device__ __forceinline__ uint32_t anew(uint32_t v) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("" : "+v"(t));
+  asm volatile("" : "+v"(v));
 #endif
-  return t;
+  return v;
 }
+
+// The thread's number for one phase of a tile.
+__device__ __forceinline__ uint32_t thread_anew() { return anew(threadIdx.x); }
 
 // One thread's share of an operand of R rows, as Stage's of tile.hpp.
 template <int SRC, int R>
@@ -58,11 +64,12 @@ struct WideStage {
     }
   }
 
-  // A whole step straight to LDS, without a wait.  Five wait states lie between a
-  // vector instruction's write of a scalar register (the buffer's) and a load that
-  // reads it, one between the write of m0 and the load; nothing else in these
-  // kernels uses m0.
-  __device__ __forceinline__ void ahead(const char* base, char* lds) const {
+  // Pieces first .. first + n - 1 of a whole step straight to LDS, without a wait.
+  // Five wait states lie between a vector instruction's write of a scalar register
+  // (the buffer's) and a load that reads it, one between the write of m0 and the
+  // load; nothing else in these kernels uses m0.
+  __device__ __forceinline__ void ahead(int wave, const char* base, char* lds, int first = 0,
+                                        int n = P) const {
 #if defined(__HIP_DEVICE_COMPILE__)
     typedef __attribute__((address_space(3))) char* lp;
     typedef int i4 __attribute__((ext_vector_type(4)));
@@ -70,14 +77,14 @@ struct WideStage {
     const i4 r = {(int)__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
                   (int)__builtin_amdgcn_readfirstlane((int)((uint32_t)(b >> 32) & 0xFFFFu)), -1,
                   0x00027000};
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t to = (uint32_t)(uintptr_t)(lp)lds + wave * 1024u;
 #pragma unroll
     for (int p = 0; p < P; ++p)
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                   :
-                   : "s"(to + p * kWideThreads * 16), "v"(off[p]), "s"(r)
-                   : "memory");
+      if (p >= first && p < first + n)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                     :
+                     : "s"(to + p * kWideThreads * 16), "v"(off[p]), "s"(r)
+                     : "memory");
 #endif
   }
 
@@ -101,61 +108,56 @@ struct WideStage {
 };
 
 // Where a wave's fragments lie in a step's operand, worked out once: the layouts of
-// tile.hpp for rows row0 .. row0 + 16 n - 1, row0 a multiple of 64.  What is left
-// of an address from fragment to fragment is a constant (kKRow) or one of four
-// (kKCol, four fragments).
+// tile.hpp for rows row0 .. row0 + 16 n - 1, row0 a multiple of 64 (kKCol: n = 4).
+// From fragment to fragment an address changes by a constant, added or, where the
+// layout permutes, by exclusive or.
 template <int SRC>
 struct Frags;
 
 template <>
 struct Frags<kKRow> {
-  uint32_t at[2];  // of the two halves along k
+  uint32_t at;
   __device__ __forceinline__ void init(uint32_t row0) {
     const uint32_t l = threadIdx.x & 63, r = l & 15;
-    at[0] = (row0 + r) * 128u + (((l >> 4) ^ (r & 7u)) << 4);
-    at[1] = at[0] ^ 64u;
+    at = (row0 + r) * 128u + (((l >> 4) ^ (r & 7u)) << 4);
   }
-  template <int N>
-  __device__ __forceinline__ void read(uint32_t lds, int ks, lu4 (&f)[N], int first = 0,
-                                       int n = N) const {
+  __device__ __forceinline__ lu4 read(uint32_t lds, int ks, int i) const {
 #if defined(__HIP_DEVICE_COMPILE__)
     typedef const __attribute__((address_space(3))) lu4* lp;
-    const uint32_t b = lds + at[ks];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i >= first && i < first + n) f[i] = *(lp)(b + (i - first) * 2048u);
+    return *(lp)((anew(at) ^ (ks * 64u)) + lds + i * 2048u);
+#else
+    return lu4{0u, 0u, 0u, 0u};
 #endif
   }
 };
 
 template <>
 struct Frags<kKCol> {
-  uint32_t at[4];
+  uint32_t at;
   __device__ __forceinline__ void init(uint32_t row0) {
     const uint32_t l = threadIdx.x & 63, k = (l >> 4) * 8 + ((l & 15) >> 2);
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
-      at[i] = kcol_at<kWideTile>(k, (row0 >> 4) + i) + (l & 3) * 8;
+    at = kcol_at<kWideTile>(k, row0 >> 4) + (l & 3) * 8;
   }
-  __device__ __forceinline__ void read(uint32_t lds, int ks, lu4 (&f)[4]) const {
+  __device__ __forceinline__ lu4 read(uint32_t lds, int ks, int i) const {
 #if defined(__HIP_DEVICE_COMPILE__)
     typedef __attribute__((address_space(3))) s4* lp;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = lds + at[i] + ks * (32 * kWideTile * 2);
-      const lu2 lo = __builtin_bit_cast(lu2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)b));
-      const lu2 hi = __builtin_bit_cast(
-          lu2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(b + 4 * kWideTile * 2)));
-      f[i] = lu4{lo[0], lo[1], hi[0], hi[1]};
-    }
+    const uint32_t b = (anew(at) ^ (i * 32u)) + lds + ks * (32 * kWideTile * 2);
+    const lu2 lo = __builtin_bit_cast(lu2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)b));
+    const lu2 hi = __builtin_bit_cast(
+        lu2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(b + 4 * kWideTile * 2)));
+    return lu4{lo[0], lo[1], hi[0], hi[1]};
+#else
+    return lu4{0u, 0u, 0u, 0u};
 #endif
   }
 };
 
-// Every load to LDS of this wave has landed.
+// All loads to LDS of this wave but the last LEFT have landed (loads come back in
+// order; stores between them only make the wait longer).
+template <int LEFT = 0>
 __device__ __forceinline__ void wait_loads() {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
 #endif
 }
 // Every read of LDS of this wave has returned; all waves meet.

@@ -18,7 +18,8 @@ SHAPES = [(1, 1, 1), (1, 40, 72), (1, 1600, 6400), (3, 64, 64), (7, 33, 129), (1
           (515, 777, 1001), (2000, 1000, 24), (1500, 40, 3600), (700, 1100, 513),
           # results of many tiles: more tiles than CUs, sums of one step, of a part of
           # one, of whole steps and of a remainder
-          (8200, 40, 1033), (4100, 64, 2050), (8193, 128, 1040), (2300, 777, 4000)]
+          (8200, 40, 1033), (8200, 130, 1033), (4100, 200, 2050), (8193, 128, 1040),
+          (8193, 192, 1000), (2300, 777, 4000)]
 
 
 def say(*a):
