@@ -24,14 +24,14 @@ __device__ __forceinline__ float logistic(float p, float& other) {
   return p < 0.0f ? zt : t;
 }
 
-// f(p) in place, eight values at a time: one branch on the kind.
+// f(p) in place, eight values at a time: one branch on the kind.  Without 1 - s
+// the logistic function is 1 / (1 + exp(-p)), as exact: where exp(-p) is large its
+// error is the result's, and past 2^126 the result is 0.
 __device__ __forceinline__ void gate_value(float (&v)[8], int kind) {
   if (kind == kGateSilu) {
-    float o;
-    for (int j = 0; j < 8; ++j) v[j] *= logistic(v[j], o);
+    for (int j = 0; j < 8; ++j) v[j] *= rcp_hw(1.0f + exp2_hw(-kLog2E * v[j]));
   } else if (kind == kGateSigmoid) {
-    float o;
-    for (int j = 0; j < 8; ++j) v[j] = logistic(v[j], o);
+    for (int j = 0; j < 8; ++j) v[j] = rcp_hw(1.0f + exp2_hw(-kLog2E * v[j]));
   } else {
     activate(v, kind);
   }

@@ -319,14 +319,24 @@ __device__ __forceinline__ int32_t persistent_tile(int32_t round, int32_t tiles)
 // tiles 0 and 1 are one group of 32 columns, 2 and 3 the next.
 __device__ __forceinline__ void keep16(const float (&v)[2][8], bool store, int64_t at_q,
                                        int64_t at_e, bool store_e, int8_t* q, uint8_t* e) {
-  uint32_t w[4], ex[2];
+  uint32_t w[4], ex[2], top[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t x = group_exp(max_groups(magnitude8(v[h])));
-    const float inv = inv_step_of(x), step = step_of(x);
-    w[2 * h] = quant4(v[h], inv, step, x != 255u);
-    w[2 * h + 1] = quant4(v[h] + 4, inv, step, x != 255u);
-    ex[h] = x;
+    top[h] = max_groups(magnitude8(v[h]));
+    ex[h] = group_exp(top[h]);
+  }
+  const bool held = past_range(top[0]) || past_range(top[1]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float inv = inv_step_of(ex[h]), step = step_of(ex[h]);
+    const bool finite = ex[h] != 255u;
+    if (held) {
+      w[2 * h] = quant4(v[h], inv, step, finite);
+      w[2 * h + 1] = quant4(v[h] + 4, inv, step, finite);
+    } else {
+      w[2 * h] = quant4_in(v[h], inv, finite);
+      w[2 * h + 1] = quant4_in(v[h] + 4, inv, finite);
+    }
   }
   transpose4(w);
   if (store) *reinterpret_cast<lu4*>(q + at_q) = lu4{w[0], w[1], w[2], w[3]};
@@ -334,37 +344,39 @@ __device__ __forceinline__ void keep16(const float (&v)[2][8], bool store, int64
   if (store_e) e[at_e] = (uint8_t)((threadIdx.x & 32) ? ex[1] : ex[0]);
 }
 
-// 16 results of a lane to the 16 columns from c that it holds after transposing.
+// 16 results of a lane (four of each of four tiles).  Exchanged between
+// neighbouring groups of 16 lanes each lane has eight columns of one of the first
+// two tiles and of one of the others, so that a store fills 64 bytes of a row.
 template <typename T>
-__device__ __forceinline__ void store16(const float (&v)[2][8], bool in_rows, T* row, int32_t c,
-                                        int32_t cols, bool vec) {
-  uint32_t a[4], b[4];
+__device__ __forceinline__ void store16(const float (&v)[2][8], bool in_rows, T* row, int32_t cw,
+                                        int32_t lg, int32_t cols, bool vec) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h) {
+    uint32_t a0 = pack2(v[h][0], v[h][1], (const T*)nullptr);
+    uint32_t b0 = pack2(v[h][2], v[h][3], (const T*)nullptr);
+    uint32_t a1 = pack2(v[h][4], v[h][5], (const T*)nullptr);
+    uint32_t b1 = pack2(v[h][6], v[h][7], (const T*)nullptr);
+    swap16(a0, a1);
+    swap16(b0, b1);
+    const int32_t c = cw + h * 32 + (lg & 1) * 16 + (lg >> 1) * 8;
+    const uint32_t w[4] = {a0, b0, a1, b1};
+    if (!in_rows) continue;
+    if (vec && c + 8 <= cols) {
+      *reinterpret_cast<lu4*>(row + c) = lu4{w[0], w[1], w[2], w[3]};
+    } else {
+      uint16_t* p = reinterpret_cast<uint16_t*>(row + c);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      a[2 * h + i] = pack2(v[h][4 * i], v[h][4 * i + 1], (const T*)nullptr);
-      b[2 * h + i] = pack2(v[h][4 * i + 2], v[h][4 * i + 3], (const T*)nullptr);
-    }
-  transpose4(a);
-  transpose4(b);
-  if (!in_rows || c >= cols) return;
-  if (vec && c + 16 <= cols) {
-    reinterpret_cast<lu4*>(row + c)[0] = lu4{a[0], b[0], a[1], b[1]};
-    reinterpret_cast<lu4*>(row + c)[1] = lu4{a[2], b[2], a[3], b[3]};
-  } else {
-    uint16_t* p = reinterpret_cast<uint16_t*>(row + c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (c + 4 * i < cols) p[4 * i] = (uint16_t)a[i];
-      if (c + 4 * i + 1 < cols) p[4 * i + 1] = (uint16_t)(a[i] >> 16);
-      if (c + 4 * i + 2 < cols) p[4 * i + 2] = (uint16_t)b[i];
-      if (c + 4 * i + 3 < cols) p[4 * i + 3] = (uint16_t)(b[i] >> 16);
+      for (int i = 0; i < 4; ++i) {
+        if (c + 2 * i < cols) p[2 * i] = (uint16_t)w[i];
+        if (c + 2 * i + 1 < cols) p[2 * i + 1] = (uint16_t)(w[i] >> 16);
+      }
     }
   }
 }
 
-template <typename T, GatedKind KIND>
+// GATE: the gate function, the identity's number also for relu (the epilogue is
+// unrolled, and all six in it would fill the instruction cache).
+template <typename T, GatedKind KIND, int GATE>
 __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tiles t) {
   constexpr bool FWD = KIND == GatedKind::kForward;
   constexpr int ASRC = FWD ? kKRow : kKCol;
@@ -548,37 +560,41 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
     const int32_t cl = cw + lg * 16;  // the lane's columns after transposing
     const bool edge = cw + 64 > a.cols;
     const bool vec = FWD || a.cols % 8 == 0;
-    // kept pre-activations of the row's 16 columns, a row of tiles ahead
-    lu4 kp, ku;
-    uint32_t ep[2], eu[2];
-    auto load_pre = [&](int j) __attribute__((always_inline)) {
+    const int gate = GATE == kActNone ? min(a.gate, kActRelu) : GATE;
+    // kept pre-activations of the row's 16 columns, two rows of tiles ahead (one
+    // ahead, each was waited for)
+    constexpr int kDeep = 3;
+    struct Pre {
+      lu4 p, u;
+      uint32_t ep[2], eu[2];
+    } pre[FWD ? 1 : kDeep];
+    auto load_pre = [&](int j, Pre& k) __attribute__((always_inline)) {
       const int64_t r = min((int64_t)rt + (wb * TB + j) * 16 + (l & 15), a.rows - 1);
-      const int64_t g = r * groups + min(cl / kAct8Group, (int32_t)groups - 1);
-      const int64_t at = g * kAct8Group + (cl & 16);
-      kp = *reinterpret_cast<const lu4*>(global(a.qp) + at);
-      ku = *reinterpret_cast<const lu4*>(global(a.qu) + at);
+      const int32_t last = (int32_t)groups - 1;
+      const int64_t at = (r * groups + min(cl / kAct8Group, last)) * kAct8Group + (cl & 16);
+      k.p = *reinterpret_cast<const lu4*>(global(a.qp) + at);
+      k.u = *reinterpret_cast<const lu4*>(global(a.qu) + at);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t gg = r * groups + min(cw / kAct8Group + h, (int32_t)groups - 1);
-        ep[h] = global(a.ep)[gg];
-        eu[h] = global(a.eu)[gg];
+        const int64_t gg = r * groups + min(cw / kAct8Group + h, last);
+        k.ep[h] = global(a.ep)[gg];
+        k.eu[h] = global(a.eu)[gg];
       }
     };
-    if constexpr (!FWD) load_pre(0);
-#pragma unroll 1
-    for (int j = 0; j < TB; ++j) {
+    if constexpr (!FWD) {
+#pragma unroll
+      for (int j = 0; j < kDeep; ++j) load_pre(j, pre[j]);
+    }
+    wait_loads();  // the next tile's steps, before stores that would be waited for
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {  // the results of 16 rows
       const int64_t r = (int64_t)rt + (wb * TB + j) * 16 + (l & 15);
       const bool in_rows = r < a.rows;
-      // the accumulators of this j, by constant indexes
+      T* row = global(static_cast<T*>(a.c)) + r * a.ldc;
       float x[TA / 2][8];
 #pragma unroll
-      for (int jj = 0; jj < TB; ++jj) {
-        if (jj > 0 && jj != j) continue;
-#pragma unroll
-        for (int i = 0; i < TA; ++i)
-          for (int m = 0; m < 4; ++m) x[i / 2][i % 2 * 4 + m] = acc[i][jj][m];
-      }
-      T* row = global(static_cast<T*>(a.c)) + r * a.ldc;
+      for (int i = 0; i < TA; ++i)
+        for (int m = 0; m < 4; ++m) x[i / 2][i % 2 * 4 + m] = acc[i][j][m];
       if constexpr (FWD) {
         if (edge) {  // columns past the last are kept as 0
 #pragma unroll
@@ -591,14 +607,13 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
         const int64_t at_e = r * groups + cl / kAct8Group;
         const int64_t at_q = at_e * kAct8Group + (cl & 16);
         const bool in = in_rows && cl / kAct8Group < groups, in_e = in && (lg & 1) == 0;
-        if (j == 0) wait_loads();  // the next tile's steps, before stores that would be waited for
         if (a.qp) {
           keep16(p, in, at_q, at_e, in_e, global(a.qp), global(a.ep));
           keep16(u, in, at_q, at_e, in_e, global(a.qu), global(a.eu));
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          gate_value(p[h], a.gate);
+          gate_value(p[h], gate);
           for (int m = 0; m < 8; ++m) p[h][m] *= u[h][m];
         }
         if (a.q) {  // as rounded: what reading y and encoding it would give
@@ -607,30 +622,34 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
           for (int h = 0; h < 2; ++h) unpack(pack(p[h], (const T*)nullptr), y[h], (const T*)nullptr);
           keep16(y, in, at_q, at_e, in_e, global(a.q), global(a.e));
         }
-        store16<T>(p, in_rows, row, cl, a.cols, vec);
+        store16<T>(p, in_rows, row, cw, lg, a.cols, vec);
       } else {
         float (&d)[2][8] = reinterpret_cast<float (&)[2][8]>(x[0]);
-        uint32_t wp[4] = {kp[0], kp[1], kp[2], kp[3]}, wu[4] = {ku[0], ku[1], ku[2], ku[3]};
-        const float sp[2] = {step_of(ep[0]), step_of(ep[1])};
-        const float su[2] = {step_of(eu[0]), step_of(eu[1])};
-        if (j + 1 < TB) load_pre(j + 1);
-        if (j == 0) wait_loads();
+        Pre& k = pre[j % kDeep];
+        uint32_t wp[4] = {k.p[0], k.p[1], k.p[2], k.p[3]};
+        uint32_t wu[4] = {k.u[0], k.u[1], k.u[2], k.u[3]};
+        const float sp[2] = {step_of(k.ep[0]), step_of(k.ep[1])};
+        const float su[2] = {step_of(k.eu[0]), step_of(k.eu[1])};
+        if (j + kDeep < TB) load_pre(j + kDeep, k);
         transpose4(wp);
         transpose4(wu);
         float f[2][8], df[2][8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int m = 0; m < 8; ++m) f[h][m] = dequant(wp[2 * h + m / 4], m % 4, sp[h]);
-          gate_both(f[h], df[h], a.gate);
+          float u[8];
+          dequant4(wp[2 * h], sp[h], f[h]);
+          dequant4(wp[2 * h + 1], sp[h], f[h] + 4);
+          dequant4(wu[2 * h], su[h], u);
+          dequant4(wu[2 * h + 1], su[h], u + 4);
+          gate_both(f[h], df[h], gate);
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
-            df[h][m] *= d[h][m] * dequant(wu[2 * h + m / 4], m % 4, su[h]);
+            df[h][m] *= d[h][m] * u[m];
             f[h][m] *= d[h][m];
           }
         }
-        store16<T>(df, in_rows, row, cl, a.cols, true);
-        store16<T>(f, in_rows, row + a.cols, cl, a.cols, vec);
+        store16<T>(df, in_rows, row, cw, lg, a.cols, true);
+        store16<T>(f, in_rows, row + a.cols, cw, lg, a.cols, vec);
       }
     }
     if (next < 0) break;
@@ -720,8 +739,15 @@ void product(const Gated& a, hipStream_t st) {
   if (wide(KIND, a.rows, a.cols, a.k)) {
     constexpr int32_t c = KIND == GatedKind::kForward ? kWideTile / 2 : kWideTile;
     const Tiles t{(a.cols + c - 1) / c, (int32_t)((a.rows + kWideTile - 1) / kWideTile), 1, 0};
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gated_wide<T, KIND>), dim3(kCUs), dim3(kWideThreads), 0,
-                       st, a, t);
+    auto launch = [&](auto gate) {
+      hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gated_wide<T, KIND, gate.value>), dim3(kCUs),
+                         dim3(kWideThreads), 0, st, a, t);
+    };
+    if (a.gate == kGateSilu) launch(std::integral_constant<int, kGateSilu>{});
+    else if (a.gate == kGateSigmoid) launch(std::integral_constant<int, kGateSigmoid>{});
+    else if (a.gate == kActGelu) launch(std::integral_constant<int, kActGelu>{});
+    else if (a.gate == kActGeluTanh) launch(std::integral_constant<int, kActGeluTanh>{});
+    else launch(std::integral_constant<int, kActNone>{});
     return;
   }
   const Tiles t = choose(KIND, a.rows, a.cols, a.k);

@@ -239,13 +239,17 @@ __device__ __forceinline__ void keep(const float (&v)[kVec<T>], int8_t* q, uint8
   top = max_lanes<kAct8Group / V>(top);
   const uint32_t ex = group_exp(top);
   const float inv = inv_step_of(ex), step = step_of(ex);
+  const bool finite = ex != 255u;
+  uint32_t w[V / 4];
+  if (past_range(top)) {
+    for (int j = 0; j < V / 4; ++j) w[j] = quant4(v + 4 * j, inv, step, finite);
+  } else {
+    for (int j = 0; j < V / 4; ++j) w[j] = quant4_in(v + 4 * j, inv, finite);
+  }
   if (col >= groups * kAct8Group) return;  // a started group is written whole
   int8_t* at = q + row * (int64_t)groups * kAct8Group + col;
-  if constexpr (V == 8)
-    *reinterpret_cast<lu2*>(at) =
-        lu2{quant4(v, inv, step, ex != 255u), quant4(v + 4, inv, step, ex != 255u)};
-  else
-    *reinterpret_cast<uint32_t*>(at) = quant4(v, inv, step, ex != 255u);
+  if constexpr (V == 8) *reinterpret_cast<lu2*>(at) = lu2{w[0], w[1]};
+  else *reinterpret_cast<uint32_t*>(at) = w[0];
   if (col % kAct8Group == 0) e[row * groups + col / kAct8Group] = (uint8_t)ex;
 }
 
@@ -428,17 +432,12 @@ __device__ __forceinline__ void load_kept(const int8_t* q, const uint8_t* e, int
   }
 }
 
-// The values: a byte with its sign bit turned over is the integer plus 128, which
-// converts in one instruction; (u - 128) * step is exact in one more.  0 where
-// there are none.
+// The values; 0 where there are none.
 template <typename T>
 __device__ __forceinline__ void decode(bool there, lu2 q, uint32_t e, float (&v)[kVec<T>]) {
-  const float step = there ? step_of(e) : 0.0f, low = -128.0f * step;
+  const float step = there ? step_of(e) : 0.0f;
 #pragma unroll
-  for (int j = 0; j < kVec<T>; ++j) {
-    const uint32_t w = q[j / 4] ^ 0x80808080u;
-    v[j] = __builtin_fmaf((float)((w >> (8 * (j % 4))) & 0xFFu), step, low);
-  }
+  for (int j = 0; j < kVec<T> / 4; ++j) dequant4(q[j], step, v + 4 * j);
 }
 
 template <typename T, int NC, int W>

@@ -191,17 +191,14 @@ __device__ __forceinline__ uint32_t magnitude(float x) {
   return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
 }
 
-// The largest magnitude bits of eight values.  As signed integers the largest
-// is the largest positive value, as unsigned ones the most negative value if
-// there is one: two three-way maxima for two values, and no masking of signs.
+// The largest magnitude bits of eight values; a NaN is the largest (IEEE 754's
+// maximum, three operands and their signs off in one instruction).
 __device__ __forceinline__ uint32_t magnitude8(const float (&v)[8]) {
-  int32_t p = 0;
-  uint32_t m = 0;
-  for (int j = 0; j < 8; ++j) {
-    p = max(p, __builtin_bit_cast(int32_t, v[j]));
-    m = max(m, __builtin_bit_cast(uint32_t, v[j]));
-  }
-  return max((uint32_t)p, m > 0x80000000u ? m & 0x7FFFFFFFu : 0u);
+  float m = 0.0f;
+  for (int j = 0; j < 8; j += 2)
+    m = __builtin_elementwise_maximum(
+        __builtin_elementwise_maximum(__builtin_fabsf(v[j]), __builtin_fabsf(v[j + 1])), m);
+  return magnitude(m);
 }
 
 // The exponent byte of a group with largest magnitude bits `top`: the step is
@@ -219,22 +216,42 @@ __device__ __forceinline__ float inv_step_of(uint32_t e) {
   return e == 255u ? 0.0f : __builtin_bit_cast(float, (254u - e) << 23);
 }
 
-// Four integers, packed.  The values are held to 127 steps before they are
-// scaled (exactly) and rounded: adding 1.5 * 2^23 rounds to an integer, ties
-// to even, whose two's complement byte is the sum's last.
-__device__ __forceinline__ uint32_t quant4(const float* v, float inv, float step, bool finite) {
+// Four integers, packed: adding 1.5 * 2^23 to a value in steps (scaled exactly)
+// rounds it to an integer, ties to even, whose two's complement byte is the sum's
+// last.
+__device__ __forceinline__ uint32_t quant4_in(const float* v, float inv, bool finite) {
   constexpr float kRound = 12582912.0f;
   uint32_t u[4];
-  for (int j = 0; j < 4; ++j) {
-    const float x = __builtin_amdgcn_fmed3f(v[j], -127.0f * step, 127.0f * step);
-    u[j] = __builtin_bit_cast(uint32_t, __builtin_fmaf(x, inv, kRound));
-  }
+  for (int j = 0; j < 4; ++j)
+    u[j] = __builtin_bit_cast(uint32_t, __builtin_fmaf(v[j], inv, kRound));
   const uint32_t lo = __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0400u);
   const uint32_t hi = __builtin_amdgcn_perm(u[3], u[2], 0x04000c0cu);
   return finite ? lo | hi : 0u;
 }
+// The values are held to 127 steps before.
+__device__ __forceinline__ uint32_t quant4(const float* v, float inv, float step, bool finite) {
+  float x[4];
+  for (int j = 0; j < 4; ++j) x[j] = __builtin_amdgcn_fmed3f(v[j], -127.0f * step, 127.0f * step);
+  return quant4_in(x, inv, finite);
+}
+// Whether a group with these largest magnitude bits has a value that would round
+// past 127 steps: 127.5 steps of 64 to the power of two, 1.9921875.  One in some
+// hundred has, so that a wave asks for all its groups together.
+__device__ __forceinline__ bool past_range(uint32_t top) {
+  return __builtin_amdgcn_ballot_w64((top & 0x7FFFFFu) >= 0x7F0000u) != 0;
+}
 __device__ __forceinline__ float dequant(uint32_t u, int j, float step) {
   return (float)(int8_t)(u >> (8 * j)) * step;
+}
+
+// Four values: a byte with its sign bit turned over is the integer plus 128, which
+// converts in one instruction; (u - 128) * step is exact in one more (and NaN for
+// the byte 255, whose step is infinite).
+__device__ __forceinline__ void dequant4(uint32_t u, float step, float* v) {
+  const uint32_t w = u ^ 0x80808080u;
+  const float low = -128.0f * step;
+  for (int j = 0; j < 4; ++j)
+    v[j] = __builtin_fmaf((float)((w >> (8 * j)) & 0xFFu), step, low);
 }
 
 // ---- activation functions ----------------------------------------------------

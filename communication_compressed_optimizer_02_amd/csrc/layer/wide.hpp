@@ -173,6 +173,8 @@ __device__ __forceinline__ void meet() {
 
 // ---- across the four groups of 16 lanes ------------------------------------------
 // Lane group g holds row l % 16's columns 4 g .. 4 g + 3 of a 16 x 16 tile.
+// swap16 of a word each of two tiles: before, group g holds word g of both, after
+// it words 2 (g / 2) and 2 (g / 2) + 1 of tile g % 2.
 __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
