@@ -348,8 +348,8 @@ __device__ __forceinline__ void keep16(const float (&v)[2][8], bool store, int64
 // neighbouring groups of 16 lanes each lane has eight columns of one of the first
 // two tiles and of one of the others, so that a store fills 64 bytes of a row.
 template <typename T>
-__device__ __forceinline__ void store16(const float (&v)[2][8], bool in_rows, T* row, int32_t cw,
-                                        int32_t lg, int32_t cols, bool vec) {
+__device__ __forceinline__ void store16(const float (&v)[2][8], bool whole, bool in_rows, T* row,
+                                        int32_t cw, int32_t lg, int32_t cols, bool vec) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t a0 = pack2(v[h][0], v[h][1], (const T*)nullptr);
@@ -360,10 +360,11 @@ __device__ __forceinline__ void store16(const float (&v)[2][8], bool in_rows, T*
     swap16(b0, b1);
     const int32_t c = cw + h * 32 + (lg & 1) * 16 + (lg >> 1) * 8;
     const uint32_t w[4] = {a0, b0, a1, b1};
-    if (!in_rows) continue;
-    if (vec && c + 8 <= cols) {
+    if (whole) {  // the same for all lanes
       *reinterpret_cast<lu4*>(row + c) = lu4{w[0], w[1], w[2], w[3]};
-    } else {
+    } else if (in_rows && vec && c + 8 <= cols) {
+      *reinterpret_cast<lu4*>(row + c) = lu4{w[0], w[1], w[2], w[3]};
+    } else if (in_rows) {
       uint16_t* p = reinterpret_cast<uint16_t*>(row + c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -560,32 +561,31 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
     const int32_t cl = cw + lg * 16;  // the lane's columns after transposing
     const bool edge = cw + 64 > a.cols;
     const bool vec = FWD || a.cols % 8 == 0;
+    const bool whole = vec && !edge && (int64_t)rt + kWideTile <= a.rows;
     const int gate = GATE == kActNone ? min(a.gate, kActRelu) : GATE;
     // kept pre-activations of the row's 16 columns, two rows of tiles ahead (one
     // ahead, each was waited for)
     constexpr int kDeep = 3;
     struct Pre {
       lu4 p, u;
-      uint32_t ep[2], eu[2];
+      uint32_t e;  // of p's two groups and of u's, in the four groups of 16 lanes
     } pre[FWD ? 1 : kDeep];
+    const int32_t last = (int32_t)groups - 1;
     auto load_pre = [&](int j, Pre& k) __attribute__((always_inline)) {
       const int64_t r = min((int64_t)rt + (wb * TB + j) * 16 + (l & 15), a.rows - 1);
-      const int32_t last = (int32_t)groups - 1;
       const int64_t at = (r * groups + min(cl / kAct8Group, last)) * kAct8Group + (cl & 16);
       k.p = *reinterpret_cast<const lu4*>(global(a.qp) + at);
       k.u = *reinterpret_cast<const lu4*>(global(a.qu) + at);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t gg = r * groups + min(cw / kAct8Group + h, last);
-        k.ep[h] = global(a.ep)[gg];
-        k.eu[h] = global(a.eu)[gg];
-      }
+      k.e = global(lg < 2 ? a.ep : a.eu)[r * groups + min(cw / kAct8Group + (lg & 1), last)];
     };
-    if constexpr (!FWD) {
+    // the next tile's steps, before stores that would be waited for; back, the kept
+    // rows' first loads are behind them and waited for before the first store
+    if constexpr (FWD) {
+      wait_loads();
+    } else {
 #pragma unroll
       for (int j = 0; j < kDeep; ++j) load_pre(j, pre[j]);
     }
-    wait_loads();  // the next tile's steps, before stores that would be waited for
 #pragma unroll
     for (int j = 0; j < TB; ++j) {  // the results of 16 rows
       const int64_t r = (int64_t)rt + (wb * TB + j) * 16 + (l & 15);
@@ -622,14 +622,16 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
           for (int h = 0; h < 2; ++h) unpack(pack(p[h], (const T*)nullptr), y[h], (const T*)nullptr);
           keep16(y, in, at_q, at_e, in_e, global(a.q), global(a.e));
         }
-        store16<T>(p, in_rows, row, cw, lg, a.cols, vec);
+        store16<T>(p, whole, in_rows, row, cw, lg, a.cols, vec);
       } else {
         float (&d)[2][8] = reinterpret_cast<float (&)[2][8]>(x[0]);
         Pre& k = pre[j % kDeep];
         uint32_t wp[4] = {k.p[0], k.p[1], k.p[2], k.p[3]};
         uint32_t wu[4] = {k.u[0], k.u[1], k.u[2], k.u[3]};
-        const float sp[2] = {step_of(k.ep[0]), step_of(k.ep[1])};
-        const float su[2] = {step_of(k.eu[0]), step_of(k.eu[1])};
+        uint32_t ex[4];
+        spread4(k.e, ex);
+        const float sp[2] = {step_of(ex[0]), step_of(ex[1])};
+        const float su[2] = {step_of(ex[2]), step_of(ex[3])};
         if (j + kDeep < TB) load_pre(j + kDeep, k);
         transpose4(wp);
         transpose4(wu);
@@ -648,8 +650,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
             f[h][m] *= d[h][m];
           }
         }
-        store16<T>(df, in_rows, row, cw, lg, a.cols, true);
-        store16<T>(f, in_rows, row + a.cols, cw, lg, a.cols, vec);
+        store16<T>(df, whole, in_rows, row, cw, lg, a.cols, true);
+        store16<T>(f, whole, in_rows, row + a.cols, cw, lg, a.cols, vec);
       }
     }
     if (next < 0) break;

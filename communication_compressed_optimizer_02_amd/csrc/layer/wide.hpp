@@ -197,6 +197,15 @@ __device__ __forceinline__ uint32_t max_groups(uint32_t v) {
   swap32(v, w);
   return max(v, w);
 }
+// The four groups' words to all of them.
+__device__ __forceinline__ void spread4(uint32_t v, uint32_t (&w)[4]) {
+  w[0] = w[1] = v;
+  swap16(w[0], w[1]);  // groups 0, 0, 2, 2 and 1, 1, 3, 3
+  w[2] = w[0];
+  w[3] = w[1];
+  swap32(w[0], w[2]);
+  swap32(w[1], w[3]);
+}
 // Transposes words of four tiles: before, group g holds word g of tiles 0 .. 3,
 // after it words 0 .. 3 of tile g.  It is its own inverse.
 __device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
