@@ -339,7 +339,8 @@ __device__ __forceinline__ void keep16(const float (&v)[2][8], bool store, int64
     }
   }
   transpose4(w);
-  if (store) *reinterpret_cast<lu4*>(q + at_q) = lu4{w[0], w[1], w[2], w[3]};
+  if (store)
+    __builtin_nontemporal_store(lu4{w[0], w[1], w[2], w[3]}, reinterpret_cast<lu4*>(q + at_q));
   // groups of 16 lanes 0 and 2 hold tiles 0 and 2
   if (store_e) e[at_e] = (uint8_t)((threadIdx.x & 32) ? ex[1] : ex[0]);
 }
@@ -347,7 +348,9 @@ __device__ __forceinline__ void keep16(const float (&v)[2][8], bool store, int64
 // 16 results of a lane (four of each of four tiles).  Exchanged between
 // neighbouring groups of 16 lanes each lane has eight columns of one of the first
 // two tiles and of one of the others, so that a store fills 64 bytes of a row.
-template <typename T>
+// ONCE: past the caches, which hold the operands (forward, 242 -> 231 us at 16384 x
+// 1024 -> 2 x 4096; the hidden gradient, with twice the bytes, lost: 212 -> 222).
+template <typename T, bool ONCE>
 __device__ __forceinline__ void store16(const float (&v)[2][8], bool whole, bool in_rows, T* row,
                                         int32_t cw, int32_t lg, int32_t cols, bool vec) {
 #pragma unroll
@@ -361,7 +364,9 @@ __device__ __forceinline__ void store16(const float (&v)[2][8], bool whole, bool
     const int32_t c = cw + h * 32 + (lg & 1) * 16 + (lg >> 1) * 8;
     const uint32_t w[4] = {a0, b0, a1, b1};
     if (whole) {  // the same for all lanes
-      *reinterpret_cast<lu4*>(row + c) = lu4{w[0], w[1], w[2], w[3]};
+      const lu4 u = {w[0], w[1], w[2], w[3]};
+      if constexpr (ONCE) __builtin_nontemporal_store(u, reinterpret_cast<lu4*>(row + c));
+      else *reinterpret_cast<lu4*>(row + c) = u;
     } else if (in_rows && vec && c + 8 <= cols) {
       *reinterpret_cast<lu4*>(row + c) = lu4{w[0], w[1], w[2], w[3]};
     } else if (in_rows) {
@@ -622,7 +627,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
           for (int h = 0; h < 2; ++h) unpack(pack(p[h], (const T*)nullptr), y[h], (const T*)nullptr);
           keep16(y, in, at_q, at_e, in_e, global(a.q), global(a.e));
         }
-        store16<T>(p, whole, in_rows, row, cw, lg, a.cols, vec);
+        store16<T, true>(p, whole, in_rows, row, cw, lg, a.cols, vec);
       } else {
         float (&d)[2][8] = reinterpret_cast<float (&)[2][8]>(x[0]);
         Pre& k = pre[j % kDeep];
@@ -650,8 +655,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
             f[h][m] *= d[h][m];
           }
         }
-        store16<T>(df, whole, in_rows, row, cw, lg, a.cols, true);
-        store16<T>(f, whole, in_rows, row + a.cols, cw, lg, a.cols, vec);
+        store16<T, false>(df, whole, in_rows, row, cw, lg, a.cols, true);
+        store16<T, false>(f, whole, in_rows, row + a.cols, cw, lg, a.cols, vec);
       }
     }
     if (next < 0) break;
