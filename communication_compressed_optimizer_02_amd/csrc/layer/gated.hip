@@ -667,6 +667,76 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
   }
 }
 
+// ---- the forward product of few rows ----------------------------------------------
+// Up to 64 rows cost what reading w costs.  A block owns 16 columns, or 32 (a group)
+// where 8 bits are kept: their rows of the gate's weights and of the others', one
+// or two fragments each.  Its 8 waves share k in lines of 64, each wave's fragments
+// straight from memory (a line of w is used by one wave, once), all of a batch's
+// loads before its products.  The waves' sums meet in LDS, added in wave order.
+// 1 x 1600 -> 2 x 6400 (41 MB of w) takes 10.6 us, 3.9 TB/s, what the call takes on
+// the host too.
+constexpr int kFewWaves = 8;
+
+template <typename T, int NB, int NA>
+__global__ __launch_bounds__(kFewWaves * 64, 2) void k_gated_few(Gated a) {
+  constexpr int U = NB <= 2 ? 4 : 2;  // lines of a batch
+  constexpr int HC = NA * 8;          // columns of the block
+  __shared__ lf4 lds[kFewWaves][NB][NA][64];
+  const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t c0 = blockIdx.x * HC;
+  const uint16_t *aw[NA], *bx[NB];
+  for (int i = 0; i < NA; ++i) {
+    const int32_t c = min(c0 + i % (NA / 2) * 16 + (l & 15), a.cols - 1);
+    aw[i] = static_cast<const uint16_t*>(a.a) + (int64_t)(i < NA / 2 ? c : a.cols + c) * a.lda;
+  }
+  for (int j = 0; j < NB; ++j)
+    bx[j] = static_cast<const uint16_t*>(a.b) +
+            min((int64_t)(j * 16 + (l & 15)), a.rows - 1) * a.ldb;
+  lf4 acc[NA][NB];
+  for (int i = 0; i < NA; ++i)
+    for (int j = 0; j < NB; ++j) acc[i][j] = lf4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t step = kFewWaves * 64;
+  for (int64_t k0 = wave * 64; k0 < a.k; k0 += step * U) {
+    lu4 fa[U][NA][2], fb[U][NB][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t k = k0 + u * step + h * 32 + (l >> 4) * 8;
+#pragma unroll
+        for (int i = 0; i < NA; ++i) fa[u][i][h] = load_k(aw[i], k, a.k);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) fb[u][j][h] = load_k(bx[j], k, a.k);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int i = 0; i < NA; ++i)
+            acc[i][j] = mfma(fa[u][i][h], fb[u][j][h], acc[i][j], (const T*)nullptr);
+  }
+  for (int j = 0; j < NB; ++j)
+    for (int i = 0; i < NA; ++i) lds[wave][j][i][l] = acc[i][j];
+  __syncthreads();
+  // wave j finishes rows 16j .. 16j+15: NA lanes to a row, eight columns each
+  if (wave >= NB || l >= 16 * NA) return;
+  const int row = l / NA, cc = l % NA * 8;
+  const int64_t r = wave * 16 + row;
+  const int32_t c = c0 + cc;
+  float v[2][8] = {}, bp[8], bu[8];
+  load_bias(a, c, bp, bu);
+  for (int w = 0; w < kFewWaves; ++w)
+    for (int g = 0; g < 2; ++g)
+      for (int h = 0; h < 2; ++h) {
+        const lf4 x = lds[w][wave][g * (NA / 2) + cc / 16][((cc % 16) / 4 + h) * 16 + row];
+        for (int j = 0; j < 4; ++j) v[g][4 * h + j] += x[j];
+      }
+  finish_forward<T>(a, r, c, bp, bu, v[0], v[1]);
+}
+
 // ---- joining a split product ------------------------------------------------------
 // A thread adds eight columns' sums in split order and finishes them as above;
 // four lanes hold a group of 32 columns.
@@ -741,8 +811,39 @@ bool wide(GatedKind kind, int64_t rows, int32_t cols, int64_t k) {
   return (cols + c - 1) / c * ((rows + kWideTile - 1) / kWideTile) >= kCUs / 2;
 }
 
+// Whether the few-rows kernel takes a forward product: one launch and no
+// workspace, but every block walks all of k and reads all of x.  Against the split
+// tiles, us a call: 1 x 1600 -> 2 x 6400 10.7 and 15.8, 1 x 16384 -> 2 x 1024 34.9
+// and 37.7, 16 x 4096 -> 2 x 1024 14.2 and 17.6, 64 x 1024 -> 2 x 4096 9.7 and 14.6,
+// 64 x 1600 -> 2 x 6400 17.5 and 18.7; but 64 x 2048 -> 2 x 6400 22.4 and 21.0, 8 x
+// 16384 -> 2 x 1024 40.2 and 38.5, 32 x 4096 -> 2 x 6400 40.5 and 30.3.
+bool few(GatedKind kind, int64_t rows, int64_t k) {
+  return kind == GatedKind::kForward && rows <= 64 && rows * k <= 102400;
+}
+// Whether its blocks take 32 columns where they could take 16: half as many, and x
+// read half as often.  16 and 32 columns, us: 16 x 1600 -> 2 x 6400 12.7 and 11.8,
+// 64 rows 22.7 and 17.5; but 1 row 10.7 and 10.9, 64 x 1024 -> 2 x 4096 9.7 and 11.7.
+bool few_wide(const Gated& a) { return a.qp || a.q || (a.rows > 4 && a.cols >= 6144); }
+
+template <typename T, int NB>
+void product_few(const Gated& a, hipStream_t st) {
+  const dim3 block(kFewWaves * 64);
+  if (few_wide(a))
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gated_few<T, NB, 4>), dim3((a.cols + 31) / 32), block, 0,
+                       st, a);
+  else
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gated_few<T, NB, 2>), dim3((a.cols + 15) / 16), block, 0,
+                       st, a);
+}
+
 template <typename T, GatedKind KIND>
 void product(const Gated& a, hipStream_t st) {
+  if (few(KIND, a.rows, a.k)) {
+    if (a.rows <= 16) product_few<T, 1>(a, st);
+    else if (a.rows <= 32) product_few<T, 2>(a, st);
+    else product_few<T, 4>(a, st);
+    return;
+  }
   if (wide(KIND, a.rows, a.cols, a.k)) {
     constexpr int32_t c = KIND == GatedKind::kForward ? kWideTile / 2 : kWideTile;
     const Tiles t{(a.cols + c - 1) / c, (int32_t)((a.rows + kWideTile - 1) / kWideTile), 1, 0};
@@ -774,10 +875,12 @@ void join(const Gated& a, hipStream_t st) {
 }  // namespace
 
 int32_t gated_splits(GatedKind kind, int64_t rows, int32_t cols, int64_t k) {
+  if (few(kind, rows, k) || wide(kind, rows, cols, k)) return 1;
   return choose(kind, rows, cols, k).splits;
 }
 
 int64_t gated_blocks(GatedKind kind, int64_t rows, int32_t cols, int64_t k) {
+  if (few(kind, rows, k)) return (cols + 15) / 16;
   const Tiles t = choose(kind, rows, cols, k);
   return (int64_t)t.ta * t.tb * t.splits;
 }

@@ -110,6 +110,7 @@ struct Gated {
 enum class GatedKind { kForward, kHiddenGrad };
 int32_t gated_splits(GatedKind kind, int64_t rows, int32_t cols, int64_t k);
 size_t gated_workspace(GatedKind kind, int64_t rows, int32_t cols, int64_t k);
+// Blocks of the product, were all of its tiles a block (what the limits are on).
 int64_t gated_blocks(GatedKind kind, int64_t rows, int32_t cols, int64_t k);
 void launch_gated(GatedKind kind, const Gated& a, hipStream_t st);
 // Joins a split product's sums (launched after it when gated_splits > 1).
