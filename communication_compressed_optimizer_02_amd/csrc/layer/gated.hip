@@ -129,7 +129,8 @@ __device__ __forceinline__ void finish_grad(const Gated& a, int64_t r, int32_t c
 // Partial sums of a split product: [split][rows][halves][cols8].
 __device__ __forceinline__ int64_t part_cols(const Gated& a) { return (a.cols + 7) / 8 * 8; }
 
-template <typename T, GatedKind KIND, int BA, int BB, int WA, int WB>
+// A block to a tile, or to a part of its sum; the loads of STAGES - 1 steps ahead.
+template <typename T, GatedKind KIND, int BA, int BB, int WA, int WB, int STAGES>
 __global__ __launch_bounds__(WA* WB * 64, 3) void k_gated(Gated a, Tiles t) {
   constexpr int NT = WA * WB * 64;
   constexpr bool FWD = KIND == GatedKind::kForward;
@@ -137,7 +138,7 @@ __global__ __launch_bounds__(WA* WB * 64, 3) void k_gated(Gated a, Tiles t) {
   constexpr int HC = FWD ? BA / 2 : BA;  // hidden columns of a tile
   constexpr int TA = BA / WA / 16, TB = BB / WB / 16;
   constexpr int kA = BA * kBK * 2, kStageBytes = kA + BB * kBK * 2;  // of a step in LDS
-  __shared__ __align__(1024) char lds[kStageBytes];
+  __shared__ __align__(1024) char lds[STAGES * kStageBytes];
 
   const int64_t work = xcd_order(blockIdx.x, gridDim.x);
   const int32_t tiles = t.ta * t.tb;
@@ -165,10 +166,10 @@ __global__ __launch_bounds__(WA* WB * 64, 3) void k_gated(Gated a, Tiles t) {
   const char* bp = static_cast<const char*>(a.b) + ((int64_t)r0 * a.ldb + kbeg) * 2;
 
   // the operand's parts have the same offsets from their origins
-  Stage<T, ASRC, HC, NT> sa;
-  Stage<T, kKRow, BB, NT> sb;
-  sa.init(c0, a.cols, (uint32_t)a.lda, 0);
-  sb.init(r0, (int32_t)min(a.rows, (int64_t)0x7FFFFFFF), (uint32_t)a.ldb, 0);
+  AheadStage<ASRC, HC, NT> sa;
+  AheadStage<kKRow, BB, NT> sb;
+  sa.init(threadIdx.x, c0, a.cols, (uint32_t)a.lda);
+  sb.init(threadIdx.x, r0, (int32_t)min(a.rows, (int64_t)0x7FFFFFFF), (uint32_t)a.ldb);
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // uniform
   const int wa = wave % WA, wb = wave / WA;
@@ -178,49 +179,66 @@ __global__ __launch_bounds__(WA* WB * 64, 3) void k_gated(Gated a, Tiles t) {
 #pragma unroll
     for (int j = 0; j < TB; ++j) acc[i][j] = lf4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // the direct loads of a wave have landed in LDS (a barrier alone does not
-  // wait for them)
-  auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
-  auto compute = [&]() __attribute__((always_inline)) {
+  auto compute = [&](const char* at) __attribute__((always_inline)) {
 #pragma unroll
     for (int ks = 0; ks < kBK / 32; ++ks) {
       lu4 fa[TA], fb[TB];
 #pragma unroll
       for (int i = 0; i < TA; ++i) {
         if constexpr (FWD)  // the first half of a wave's tiles are p's, the others u's
-          fa[i] = fragment<kKRow, HC>(lds + (i < TA / 2 ? 0 : kA / 2),
+          fa[i] = fragment<kKRow, HC>(at + (i < TA / 2 ? 0 : kA / 2),
                                       (wa * (TA / 2) + i % (TA / 2)) * 16, ks);
         else
-          fa[i] = fragment<kKCol, HC>(lds, (wa * TA + i) * 16, ks);
+          fa[i] = fragment<kKCol, HC>(at, (wa * TA + i) * 16, ks);
       }
 #pragma unroll
-      for (int j = 0; j < TB; ++j) fb[j] = fragment<kKRow, BB>(lds + kA, (wb * TB + j) * 16, ks);
+      for (int j = 0; j < TB; ++j) fb[j] = fragment<kKRow, BB>(at + kA, (wb * TB + j) * 16, ks);
 #pragma unroll
       for (int j = 0; j < TB; ++j)
 #pragma unroll
         for (int i = 0; i < TA; ++i) acc[i][j] = mfma(fa[i], fb[j], acc[i][j], (const T*)nullptr);
     }
   };
+  // Step s lies in part s % STAGES of LDS.  A sum whose length is no multiple of the
+  // step begins with what is left over, through registers.
   const int32_t full = (int32_t)((kend - kbeg) / kBK), rest = (int32_t)((kend - kbeg) % kBK);
-  for (int32_t s = 0; s < full; ++s) {
-    if (s > 0) __syncthreads();  // every wave is done with the last step's tile
-    sa.direct(ap, lds);
-    if constexpr (FWD) sa.direct(ap2, lds + kA / 2);
-    sb.direct(bp, lds + kA);
-    ap += astep;
-    ap2 += astep;
-    bp += kBK * 2;
-    landed();
-    __syncthreads();
-    compute();
-  }
-  if (rest > 0) {
-    if (full > 0) __syncthreads();
-    sa.tail(ap, lds, rest);
-    if constexpr (FWD) sa.tail(ap2, lds + kA / 2, rest);
-    sb.tail(bp, lds + kA, rest);
-    __syncthreads();
-    compute();
+  const int32_t steps = full + (rest > 0);
+  auto issue = [&](int32_t s, int32_t part) __attribute__((always_inline)) {
+    char* to = lds + part * kStageBytes;
+    if (s == 0 && rest > 0) {
+      sa.tail(threadIdx.x, ap + full * astep, to, rest);
+      if constexpr (FWD) sa.tail(threadIdx.x, ap2 + full * astep, to + kA / 2, rest);
+      sb.tail(threadIdx.x, bp + (int64_t)full * kBK * 2, to + kA, rest);
+    } else {
+      sa.ahead(wave, ap, to);
+      if constexpr (FWD) sa.ahead(wave, ap2, to + kA / 2);
+      sb.ahead(wave, bp, to + kA);
+      ap += astep;
+      ap2 += astep;
+      bp += kBK * 2;
+    }
+  };
+  constexpr int kLoads = (FWD ? 2 : 1) * decltype(sa)::P + decltype(sb)::P;  // of a step
+  int32_t part = 0;
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s)
+    if (s < steps) issue(s, s);
+#pragma unroll 1
+  for (int32_t s = 0; s < steps; ++s) {
+    if constexpr (STAGES == 1) {
+      if (s > 0) meet();  // every wave is done with the last step
+      issue(s, 0);
+      wait_loads();
+      meet();
+    } else {
+      // step s has landed, those behind it may be on their way
+      if (s + STAGES - 2 < steps) wait_loads<(STAGES - 2) * kLoads>();
+      else wait_loads();
+      meet();  // and every wave is done with step s - 1, whose part is free
+      if (s + STAGES - 1 < steps) issue(s + STAGES - 1, part == 0 ? STAGES - 1 : part - 1);
+    }
+    compute(lds + part * kStageBytes);
+    part = part == STAGES - 1 ? 0 : part + 1;
   }
 
   // The results go through LDS, 16 rows of a wave at a time and within the
@@ -230,7 +248,7 @@ __global__ __launch_bounds__(WA* WB * 64, 3) void k_gated(Gated a, Tiles t) {
   constexpr int kCols = HC / WA;            // hidden columns of a wave
   constexpr int kLanes = kCols / 8;         // lanes of a row
   constexpr int kIter = 16 * kLanes / 64;
-  static_assert(WA * WB * 16 * kRow * 4 <= kStageBytes, "epilogue rows fit the tile");
+  static_assert(WA * WB * 16 * kRow * 4 <= STAGES * kStageBytes, "epilogue rows fit");
   static_assert(kIter >= 1 && kCols % kAct8Group == 0, "whole groups to a wave");
   const int l = threadIdx.x & 63;
   float* rows = reinterpret_cast<float*>(lds) + wave * 16 * kRow;
@@ -397,8 +415,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_gated_wide(Gated args, Tile
   const int32_t full = (int32_t)(args.k / kBK), rest = (int32_t)(args.k % kBK);
   const int32_t steps = full + (rest > 0);
 
-  WideStage<ASRC, HC> sa;
-  WideStage<kKRow, kWideTile> sb;
+  AheadStage<ASRC, HC, kWideThreads> sa;
+  AheadStage<kKRow, kWideTile, kWideThreads> sb;
   const char *ap, *ap2, *bp;  // of the step to be loaded next
   const char *rest_a, *rest_b;
   int64_t astep;
@@ -784,20 +802,29 @@ __global__ __launch_bounds__(256) void k_gated_join(Gated a, int32_t splits) {
 
 // ---- host side ----------------------------------------------------------------------
 constexpr int kCUs = 256;
-constexpr int kTile = 128;
+constexpr int kSplitBelow = kCUs / 2, kSplitLeast = 4;
+
+int64_t tiles_of(GatedKind kind, int64_t rows, int32_t cols, int32_t tile) {
+  const int32_t wide = kind == GatedKind::kForward ? tile / 2 : tile;
+  return (int64_t)((cols + wide - 1) / wide) * ((rows + tile - 1) / tile);
+}
+
+// Whether a product of few tiles of 128 x 128 is cut into tiles of 64 x 64.
+bool small(GatedKind kind, int64_t rows, int32_t cols) {
+  return tiles_of(kind, rows, cols, 128) <= kCUs;
+}
 
 Tiles choose(GatedKind kind, int64_t rows, int32_t cols, int64_t k) {
-  const int32_t wide = kind == GatedKind::kForward ? kTile / 2 : kTile;
+  const int32_t tile = small(kind, rows, cols) ? 64 : 128;
+  const int32_t wide = kind == GatedKind::kForward ? tile / 2 : tile;
   Tiles t;
   t.ta = (cols + wide - 1) / wide;
-  t.tb = (int32_t)((rows + kTile - 1) / kTile);
+  t.tb = (int32_t)((rows + tile - 1) / tile);
   const int64_t all = (int64_t)t.ta * t.tb, steps = (k + kBK - 1) / kBK;
   int64_t splits = 1;
-  if (all > 0 && all <= kCUs) {
-    const int64_t least = all <= kCUs / 2 ? 4 : 10;
-    splits = std::max<int64_t>(
-        1, std::min<int64_t>({2 * kCUs / all, steps / least, (int64_t)kMaxSplits}));
-  }
+  if (all > 0 && all <= kSplitBelow)
+    splits = std::max<int64_t>(1, std::min<int64_t>({2 * kCUs / all, steps / kSplitLeast,
+                                                     (int64_t)kMaxSplits}));
   t.ksteps = (int32_t)std::max<int64_t>(1, (steps + splits - 1) / splits);
   t.splits = (int32_t)std::max<int64_t>(1, (steps + t.ksteps - 1) / t.ksteps);
   return t;
@@ -860,8 +887,14 @@ void product(const Gated& a, hipStream_t st) {
   }
   const Tiles t = choose(KIND, a.rows, a.cols, a.k);
   const uint32_t grid = (uint32_t)gated_blocks(KIND, a.rows, a.cols, a.k);
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gated<T, KIND, kTile, kTile, 2, 2>), dim3(grid), dim3(256),
-                     0, st, a, t);
+  if (small(KIND, a.rows, a.cols)) {
+    constexpr int WA = KIND == GatedKind::kForward ? 1 : 2;
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gated<T, KIND, 64, 64, WA, 4 / WA, 3>), dim3(grid),
+                       dim3(256), 0, st, a, t);
+  } else {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gated<T, KIND, 128, 128, 2, 2, 1>), dim3(grid), dim3(256),
+                       0, st, a, t);
+  }
 }
 
 template <typename T, GatedKind KIND>

@@ -40,10 +40,11 @@ __device__ __forceinline__ uint32_t anew(uint32_t v) {
 // The thread's number for one phase of a tile.
 __device__ __forceinline__ uint32_t thread_anew() { return anew(threadIdx.x); }
 
-// One thread's share of an operand of R rows, as Stage's of tile.hpp.
-template <int SRC, int R>
-struct WideStage {
-  static constexpr int P = R * (kBK / 8) / kWideThreads;
+// One thread's share of an operand of R rows in a block of NT threads, as Stage's
+// of tile.hpp.
+template <int SRC, int R, int NT>
+struct AheadStage {
+  static constexpr int P = R * (kBK / 8) / NT;
   uint32_t off[P];  // bytes from the step's origin
 
   __device__ __forceinline__ static uint32_t k_of(uint32_t i) {
@@ -54,7 +55,7 @@ struct WideStage {
     const uint32_t last = (uint32_t)(rows - 1 - r0);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const uint32_t i = p * kWideThreads + tid, k = k_of(i);
+      const uint32_t i = p * NT + tid, k = k_of(i);
       if constexpr (SRC == kKRow) {
         off[p] = (min(i / (kBK / 8), last) * ld + k) * 2;
       } else {
@@ -83,7 +84,7 @@ struct WideStage {
       if (p >= first && p < first + n)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                      :
-                     : "s"(to + p * kWideThreads * 16), "v"(off[p]), "s"(r)
+                     : "s"(to + p * NT * 16), "v"(off[p]), "s"(r)
                      : "memory");
 #endif
   }
@@ -93,7 +94,7 @@ struct WideStage {
                                        int32_t left) const {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int32_t k = (int32_t)k_of(p * kWideThreads + tid);
+      const int32_t k = (int32_t)k_of(p * NT + tid);
       lu4 u = {0u, 0u, 0u, 0u};
       if (k < left) {
         u = *reinterpret_cast<const lu4*>(global(base) + off[p]);
@@ -102,7 +103,7 @@ struct WideStage {
             u[j] &= (k + 2 * j < left ? 0xFFFFu : 0u) | (k + 2 * j + 1 < left ? 0xFFFF0000u : 0u);
         }
       }
-      *reinterpret_cast<lu4*>(lds + (p * kWideThreads + tid) * 16) = u;
+      *reinterpret_cast<lu4*>(lds + (p * NT + tid) * 16) = u;
     }
   }
 };
