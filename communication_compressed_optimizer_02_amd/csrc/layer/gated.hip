@@ -809,9 +809,14 @@ int64_t tiles_of(GatedKind kind, int64_t rows, int32_t cols, int32_t tile) {
   return (int64_t)((cols + wide - 1) / wide) * ((rows + tile - 1) / tile);
 }
 
-// Whether a product of few tiles of 128 x 128 is cut into tiles of 64 x 64.
+// Whether a product of few tiles of 128 x 128 is cut into tiles of 64 x 64.  In us,
+// 128 and 64: 515 x 777 -> 2 x 1001 (80 tiles) 21.3 and 14.3, 256 x 1600 -> 2 x 6400
+// (200) 35.3 and 25.6; but 2048 x 1024 -> 2 x 2048 (512 tiles) 24.2 and 32.9; the hidden
+// gradient of 1500 x 1600 -> 3200 (300 tiles) 45.0 and 35.2, of 4096 x 1024 -> 2048
+// (512) 38.4 and 42.1.
 bool small(GatedKind kind, int64_t rows, int32_t cols) {
-  return tiles_of(kind, rows, cols, 128) <= kCUs;
+  return tiles_of(kind, rows, cols, 128) <=
+         (kind == GatedKind::kForward ? kCUs : kCUs + kCUs / 2);
 }
 
 Tiles choose(GatedKind kind, int64_t rows, int32_t cols, int64_t k) {
@@ -830,12 +835,19 @@ Tiles choose(GatedKind kind, int64_t rows, int32_t cols, int64_t k) {
   return t;
 }
 
-// Whether the tiles of 256 x 256 give every CU work, and sums have the two whole
-// steps that are loaded ahead.
+// Whether the tiles of 256 x 256 are taken: sums of the two whole steps that are
+// loaded ahead, and rounds of one tile to a CU that leave few CUs without one.  In
+// us, 128 x 128 and 256 x 256: 4096 x 1024 -> 2 x 4096 (2 full rounds) 80 and 68, 6000
+// x 1000 -> 2 x 4300 (4 rounds, 80 % full) 149 and 133, 2600 x 300 -> 2 x 2600 (1
+// round, 90 %) 26.5 and 22.6, 3000 x 2000 -> 2 x 1500 (1 round, 56 %) 62 and 50; but
+// 4096 x 1024 -> 2 x 3000 (2 rounds, 75 %) 60 and 66, 4096 x 1024 -> 2 x 1024 (1, 50
+// %) 24 and 28; the hidden gradient of 4096 x 1024 -> 3000 (1 round, 75 %) 58 and 49,
+// of 4096 x 4000 -> 2300 (1, 56 %) 124 and 130.
 bool wide(GatedKind kind, int64_t rows, int32_t cols, int64_t k) {
   if (k < 2 * kBK) return false;
-  const int64_t c = kind == GatedKind::kForward ? kWideTile / 2 : kWideTile;
-  return (cols + c - 1) / c * ((rows + kWideTile - 1) / kWideTile) >= kCUs / 2;
+  const int64_t t = tiles_of(kind, rows, cols, kWideTile), rounds = (t + kCUs - 1) / kCUs;
+  if (rounds > 1) return t * 100 >= rounds * kCUs * 77;
+  return t >= kCUs * 3 / 4 || (kind == GatedKind::kForward && t > kCUs / 2 && k >= 1536);
 }
 
 // Whether the few-rows kernel takes a forward product: one launch and no

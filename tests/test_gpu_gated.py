@@ -16,10 +16,10 @@ TWO = ("f16", "bf16")
 SHAPES = [(1, 1, 1), (1, 40, 72), (1, 1600, 6400), (3, 64, 64), (7, 33, 129), (16, 5000, 16),
           (33, 520, 200), (64, 4096, 100), (130, 200, 77), (128, 128, 128), (257, 72, 400),
           (515, 777, 1001), (2000, 1000, 24), (1500, 40, 3600), (700, 1100, 513),
-          # results of many tiles: more tiles than CUs, sums of one step, of a part of
-          # one, of whole steps and of a remainder
-          (8200, 40, 1033), (8200, 130, 1033), (4100, 200, 2050), (8193, 128, 1040),
-          (8193, 192, 1000), (2300, 777, 4000)]
+          # results of many tiles: more tiles than CUs and fewer, sums of less than a step,
+          # of whole steps and with a remainder
+          (8200, 40, 1033), (2300, 777, 4000), (8200, 130, 1700), (4100, 200, 3300),
+          (8193, 128, 1700), (8193, 192, 3400)]
 
 
 def say(*a):
