@@ -16,11 +16,21 @@
 //   dgamma = sum dz * h, dbeta = sum dz, S = sum e * k, T = sum e:
 //   dgamma_b = gate * S, dbeta_b = gate * T, dgate = gamma_b * S + beta_b * T
 //
-// A row is read once into registers: eight columns a lane, by 1 to 16 waves (16
-// columns a lane above 8192).  A block walks many rows, so parameters are read
-// once and the column sums stay in binary32 registers until its last row; they
-// are written as partial sums and added per column in binary64 in a fixed
-// order.
+// A row is read once into registers: eight columns a lane, by as many waves as it
+// has 512 columns (16 columns a lane above 8192).  A block walks many rows, so
+// parameters are read once and the column sums stay in binary32 until its last
+// row; they are written as partial sums and added per column in binary64 in a
+// fixed order.
+//
+// Bound by the memory and, nearly as much, by the vector unit: a wave's 512 columns
+// take 630 instructions forward with both norms, dropout and both kept forms (a
+// sixth of them the random bits, whose 32-bit products are four times as long), 78 %
+// of the unit's time at 32768 x 1024.  So waves without columns are what costs most:
+// with the waves a row rounded up to 1, 2, 4, 8 or 16, 33.5 million bfloat16 elements
+// of 2500 columns took 157 us, of 4500 199 us, and 93 and 136 with the waves counted
+// out.  Measured, both norms, dropout, all kept, bfloat16: 32768 x 1024 84 us (4.0
+// TB/s), 8192 x 4096 81 us (4.2 TB/s), back 80 and 89 us; binary32, the RMS norm of
+// 2048 x 8192 58 us (5.0 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -36,44 +46,105 @@ namespace oba {
 
 namespace {
 
-// W waves to a row; blocks of 8 waves hold 8 / W rows at a time, 16 waves one.
-template <int W>
-constexpr int kThreads = W == 16 ? 1024 : 512;
-template <int W>
-constexpr int kRows = kThreads<W> / 64 / W;
+// Columns of a wave: 8 a lane, or 16 where a row has more than 16 such waves.
+// Rows of one wave, ONE, need no exchange.
+template <typename T, int NC>
+constexpr int32_t kWaveCols = NC * kVec<T> * 64;
 
-// Sums of two values over a row's W waves: every lane gets them, added in wave
-// order.  One barrier: two calls in turn use the two halves of `lds`, and a wave
-// that writes a half again has passed the barrier of the call between, behind
-// every wave's reads of this half.  All waves of a block call it together.
-template <int W, typename F>
-__device__ __forceinline__ void row_sums(F& a, F& b, F (*lds)[2][kThreads<W> / 64], int& half) {
-  a = wave_sum(a);
-  b = wave_sum(b);
-  if constexpr (W > 1) {
-    const int w = threadIdx.x >> 6, first = w & ~(W - 1);
-    if ((threadIdx.x & 63) == 0) {
-      lds[half][0][w] = a;
-      lds[half][1][w] = b;
-    }
-    __syncthreads();
-    a = b = 0;
-#pragma unroll 4
-    for (int i = 0; i < W; ++i) {
-      a += lds[half][0][first + i];
-      b += lds[half][1][first + i];
-    }
-    half ^= 1;
-  }
+// Rows to a block: forward, eight of one wave, else one (its waves wait for no
+// other row's).  Backward, where a block's rows share one partial sum, eight waves'
+// if they are whole rows, else what 16 waves hold: fewer partial sums, but all wait
+// for one another (1600 columns: 91 us against 100 with 16; 2500: 132 against 95,
+// 4096: 97 against 88, for 2^25 elements).
+template <bool BACK>
+__host__ __device__ inline int32_t block_rows(int32_t waves) {
+  if (!BACK) return waves == 1 ? 8 : 1;
+  return waves == 1 || waves == 2 || waves == 4 ? 8 / waves : 16 / waves;
 }
 
-// Columns of a row that its wave w holds.
-template <typename T, int NC, int W>
-__device__ __forceinline__ int32_t wave_cols(int32_t w, int32_t cols) {
-  int32_t n = 0;
+// Where a lane's columns lie: chunk c at `at` + c * `step`; its wave is number
+// `wave` of the `waves` of the block's row number `row`, whose first wave is
+// `first`.  All but `at` is the same for a wave's lanes.
+template <typename T, int NC, bool ONE>
+struct Where {
+  int32_t waves, wave, first, row, at, step;
+  __device__ __forceinline__ explicit Where(int32_t cols) {
+    const int32_t w = __builtin_amdgcn_readfirstlane((int32_t)threadIdx.x >> 6);
+    waves = ONE ? 1 : (cols + kWaveCols<T, NC> - 1) / kWaveCols<T, NC>;
+    row = ONE ? w : __builtin_amdgcn_readfirstlane(w / waves);
+    first = row * waves;
+    wave = w - first;
+    at = (wave * 64 + ((int32_t)threadIdx.x & 63)) * kVec<T>;
+    step = waves * 64 * kVec<T>;
+  }
+  __device__ __forceinline__ int32_t col(int c) const { return at + c * step; }
+  // columns of the row that its wave w holds
+  __device__ __forceinline__ int32_t part(int32_t w, int32_t cols) const {
+    int32_t n = 0;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) n += min(max(cols - (c * W + w) * 64 * kVec<T>, 0), 64 * kVec<T>);
-  return n;
+    for (int c = 0; c < NC; ++c)
+      n += min(max(cols - c * step - w * 64 * kVec<T>, 0), 64 * kVec<T>);
+    return n;
+  }
+};
+
+// Over the waves of a row: each wave's two values are laid into LDS, and lane i of
+// every 16 takes wave i's, so that sums over the waves are four exchanges however
+// many waves there are.  One barrier: two meetings in turn use the two halves of
+// `lds`, and a wave that writes a half again has passed the barrier of the meeting
+// between, behind every wave's reads of this half.  All waves of a block meet
+// together.
+template <typename F>
+using Meet = F __attribute__((ext_vector_type(2)));
+
+template <typename T, int NC, typename F>
+__device__ __forceinline__ Meet<F> meet(F a, F b, const Where<T, NC, false>& at,
+                                        Meet<F> (*lds)[16], int& half) {
+  if ((threadIdx.x & 63) == 0) lds[half][at.first + at.wave] = Meet<F>{a, b};
+  __syncthreads();
+  const int32_t i = (int32_t)threadIdx.x & 15;
+  Meet<F> v = lds[half][at.first + min(i, at.waves - 1)];
+  half ^= 1;
+  if (i >= at.waves) v[1] = 0;
+  return v;
+}
+// The sum of 16 neighbouring lanes, in all of them.
+__device__ __forceinline__ float sum16(float v) {
+  v += dppf<kXor1>(v);
+  v += dppf<kXor2>(v);
+  v += dppf<kHalfMirror>(v);
+  return v + dppf<kMirror>(v);
+}
+__device__ __forceinline__ double sum16(double v) {
+  v += dppd<kXor1>(v);
+  v += dppd<kXor2>(v);
+  v += dppd<kHalfMirror>(v);
+  return v + dppd<kMirror>(v);
+}
+
+// The sum of a wave's 64 lanes, in all of them: rows of 16 by exchanges, then the
+// first row's sum to the second and the third's to the fourth, and the second's to
+// the fourth, whose last lane has it all: 7 instructions.
+__device__ __forceinline__ float wave_total(float v) {
+  v = sum16(v);
+  auto from = [](float x, auto row, auto mask) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+        0, __builtin_bit_cast(int, x), decltype(row)::value, decltype(mask)::value, 0xF, false));
+  };
+  v += from(v, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});
+  v += from(v, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// 1 / sqrt(v): the estimate, one unit off, and one step of Newton's method; small
+// values are scaled into the range of normal ones.
+__device__ __forceinline__ float inv_root(float v) {
+  const bool tiny = v < 0x1p-100f;
+  v = tiny ? v * 0x1p100f : v;
+  float y = __builtin_amdgcn_rsqf(v);
+  const float e = __builtin_fmaf(-v * y, y, 1.0f);
+  if (v > 0.0f && v < __builtin_inff()) y = __builtin_fmaf(0.5f * y, e, y);
+  return tiny ? y * 0x1p50f : y;
 }
 
 // What a norm divides by: columns of the row and of the lane's wave, with their
@@ -106,9 +177,10 @@ __device__ __forceinline__ float quotient(float s, float n, float inv) {
 // n.  For binary32 rows the first sum is binary64 and the second needs no mean:
 // a row of one value, whose sum binary32 does not hold, is then centred to 0.  For
 // 16-bit rows (and r made of them) binary32 does.
-template <typename T, int NC, int W>
+template <typename T, int NC, bool ONE>
 __device__ __forceinline__ void wave_moments(const float (&v)[NC][kVec<T>], int32_t cols,
-                                             const Share& part, double& mean, double& squares) {
+                                             const Where<T, NC, ONE>& at, const Share& part,
+                                             double& mean, double& squares) {
   constexpr int V = kVec<T>;
   float m;
   if constexpr (V == 4) {
@@ -125,13 +197,13 @@ __device__ __forceinline__ void wave_moments(const float (&v)[NC][kVec<T>], int3
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) s += v[c][j];
-    m = quotient(wave_sum(s), (float)part.n, (float)part.inv);
+    m = quotient(wave_total(s), (float)part.n, (float)part.inv);
   }
   float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     // lanes that hold none of the row, and elements past its end, add nothing
-    const int32_t col = chunk_col<T, W>(c);
+    const int32_t col = at.col(c);
     const float mc = col < cols ? m : 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -141,9 +213,9 @@ __device__ __forceinline__ void wave_moments(const float (&v)[NC][kVec<T>], int3
       s2 = __builtin_fmaf(t, t, s2);
     }
   }
-  squares = (double)wave_sum(s2);
+  squares = (double)wave_total(s2);
   if constexpr (V == 8) {
-    const double d = (double)wave_sum(s1);
+    const double d = (double)wave_total(s1);
     mean = __builtin_fma(d, part.inv, (double)m);
     squares = __builtin_fma(-d * part.inv, d, squares);
   }
@@ -151,37 +223,34 @@ __device__ __forceinline__ void wave_moments(const float (&v)[NC][kVec<T>], int3
 
 // Rows to their normalised form in place; the reciprocal of the spread.  The
 // waves' squares are moved to the row's mean, n_w (mean_w - mean)^2 for each, so
-// that one exchange between the waves serves mean and spread.
-template <typename T, int NC, int W>
-__device__ __forceinline__ float normalise(float (&v)[NC][kVec<T>], int32_t cols, int kind,
-                                           float eta, const Share& row, const Share& part, double (*lds)[2][kThreads<W> / 64],
-                                           int& half) {
+// that one meeting serves mean and spread; their means are taken as differences
+// from the first wave's.  n: the columns of the wave whose values the lane takes.
+template <typename T, int NC, bool ONE>
+__device__ __forceinline__ float normalise(float (&v)[NC][kVec<T>], int32_t cols,
+                                           const Where<T, NC, ONE>& at, int kind, float eta,
+                                           const Share& row, const Share& part, float n,
+                                           Meet<double> (*lds)[16], int& half) {
   constexpr int V = kVec<T>;
-  const int wave = threadIdx.x >> 6, first = wave & ~(W - 1);
   double squares;
   float mu = 0.0f, off = 0.0f;
   if (kind == kNormLayer) {
     double mean;
-    wave_moments<T, NC, W>(v, cols, part, mean, squares);
-    if constexpr (W > 1) {
-      if ((threadIdx.x & 63) == 0) {
-        lds[half][0][wave] = mean;
-        lds[half][1][wave] = squares;
+    wave_moments(v, cols, at, part, mean, squares);
+    if constexpr (!ONE) {
+      const Meet<double> m = meet(mean, squares, at, lds, half);
+      const double from = lane_of(m[0], 0);
+      float apart;
+      if constexpr (V == 4) {
+        const double d = m[0] - from;
+        const double moved = quotient(sum16((double)n * d), row.n, row.inv);
+        mean = from + moved;
+        apart = (float)(d - moved);
+      } else {  // the waves' sums are binary32's already
+        const float inv = (float)row.inv, d = (float)(m[0] - from), moved = sum16(n * d) * inv;
+        apart = d - moved;
+        mean = from + ((double)moved + (double)(sum16(n * apart) * inv));
       }
-      __syncthreads();
-      double all = 0.0;
-#pragma unroll 4
-      for (int i = 0; i < W; ++i)
-        all = __builtin_fma((double)wave_cols<T, NC, W>(i, cols), lds[half][0][first + i], all);
-      mean = quotient(all, row.n, row.inv);
-      squares = 0.0;
-#pragma unroll 4
-      for (int i = 0; i < W; ++i) {
-        const double n = (double)wave_cols<T, NC, W>(i, cols);
-        const double d = lds[half][0][first + i] - mean;
-        squares += __builtin_fma(n * d, d, lds[half][1][first + i]);
-      }
-      half ^= 1;
+      squares = (double)sum16(__builtin_fmaf(n * apart, apart, (float)m[1]));
     }
     mu = (float)mean;
     off = (float)(mean - (double)mu);
@@ -191,26 +260,19 @@ __device__ __forceinline__ float normalise(float (&v)[NC][kVec<T>], int32_t cols
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) s2 = __builtin_fmaf(v[c][j], v[c][j], s2);
-    s2 = wave_sum(s2);
+    s2 = wave_total(s2);
     squares = (double)s2;
-    if constexpr (W > 1) {
-      if ((threadIdx.x & 63) == 0) lds[half][0][wave] = squares;
-      __syncthreads();
-      squares = 0.0;
-#pragma unroll 4
-      for (int i = 0; i < W; ++i) squares += lds[half][0][first + i];
-      half ^= 1;
-    }
+    if constexpr (!ONE) squares = (double)sum16((float)meet(0.0, squares, at, lds, half)[1]);
   }
-  const float rs = 1.0f / __builtin_sqrtf((float)(squares * row.inv) + eta);
+  const float rs = inv_root((float)(squares * row.inv) + eta);
   if (kind == kNormLayer) {
     const float low = -off * rs;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
 #pragma unroll
       for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(v[c][j] - mu, rs, low);
-      if (cols % (NC * W * 64 * V) != 0) {  // 0 stays past the row's end
-        const int32_t col = chunk_col<T, W>(c);
+      if (cols != at.waves * kWaveCols<T, NC>) {  // 0 stays past the row's end
+        const int32_t col = at.col(c);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[c][j] = col + j < cols ? v[c][j] : 0.0f;
       }
@@ -257,7 +319,7 @@ __device__ __forceinline__ void keep(const float (&v)[kVec<T>], int8_t* q, uint8
 // past the last column.  Rows of 8 columns a lane hold them in registers from row
 // to row; at 16 columns a lane they are read again for each row (from cache): held
 // they spilled.
-template <typename T, int NC, int W>
+template <typename T, int NC, bool ONE>
 struct Params {
   static constexpr int V = kVec<T>;
   static constexpr bool kHold = NC * V <= 8;
@@ -265,8 +327,7 @@ struct Params {
   float other;
   float held[kHold ? NC : 1][V];
 
-  __device__ __forceinline__ void read(int c, int32_t cols, float (&v)[V]) const {
-    const int32_t col = chunk_col<T, W>(c);
+  __device__ __forceinline__ void read(int32_t col, int32_t cols, float (&v)[V]) const {
 #pragma unroll
     for (int j = 0; j < V; j += 4) {
       if (!p) {
@@ -279,19 +340,21 @@ struct Params {
       }
     }
   }
-  __device__ __forceinline__ Params(const float* from, float without, int32_t cols)
+  __device__ __forceinline__ Params(const float* from, float without, int32_t cols,
+                                    const Where<T, NC, ONE>& at)
       : p(from), other(without) {
     if constexpr (kHold) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) read(c, cols, held[c]);
+      for (int c = 0; c < NC; ++c) read(at.col(c), cols, held[c]);
     }
   }
-  __device__ __forceinline__ void get(int c, int32_t cols, float (&v)[V]) const {
+  __device__ __forceinline__ void get(int c, int32_t col, int32_t cols,
+                                      float (&v)[V]) const {
     if constexpr (kHold) {
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] = held[c][j];
     } else {
-      read(c, cols, v);
+      read(col, cols, v);
     }
   }
 };
@@ -302,40 +365,37 @@ constexpr int kWaves = 4;
 template <typename T, int NC>
 constexpr bool kAhead = NC * kVec<T> <= 8;
 
-// The row of a block's first round that a wave belongs to, the same for all its
-// lanes: addresses of rows then need no vector registers.
-template <int W>
-__device__ __forceinline__ int32_t wave_row() {
-  return __builtin_amdgcn_readfirstlane((int32_t)threadIdx.x / (W * 64));
-}
-
-template <typename T, int NC, int W>
-__global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_fwd(JoinFwd args) {
+template <typename T, int NC, bool ONE>
+__global__ __launch_bounds__(1024, kWaves) void k_join_fwd(JoinFwd args) {
   JoinFwd a = arguments(args);
-  constexpr int V = kVec<T>, R = kRows<W>;
-  __shared__ double lds[2][2][kThreads<W> / 64];
+  constexpr int V = kVec<T>;
+  __shared__ Meet<double> lds[2][16];
   int half = 0;
   const int32_t cols = a.cols, groups = (cols + kAct8Group - 1) / kAct8Group;
+  const Where<T, NC, ONE> at(cols);
+  const int32_t R = block_rows<false>(at.waves);
   const int64_t rows = a.rows, stride = (int64_t)gridDim.x * R;
-  const bool first_lane = (threadIdx.x & (W * 64 - 1)) == 0;
+  const bool first_lane = at.at == 0;
   const RngKey key = load_key(a.drop);
-  int64_t r = (int64_t)blockIdx.x * R + wave_row<W>();
+  int64_t r = (int64_t)blockIdx.x * R + at.row;
   constexpr bool A = kAhead<T, NC>;  // each loaded anew once the row before is taken out of it
   lu4 nx[NC], nb[NC];
   auto load = [&](const void* from, int64_t ld, int64_t row, lu4 (&to)[NC]) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-      to[c] = load_raw(global(static_cast<const T*>(from)) + row * ld, chunk_col<T, W>(c), cols);
+      to[c] = load_raw(global(static_cast<const T*>(from)) + row * ld, at.col(c), cols);
   };
   if (A && r < a.rows) {
     load(a.x, a.ldx, r, nx);
     if (a.b) load(a.b, a.ldb, r, nb);
   }
-  const Params<T, NC, W> gate(global(a.gate), 1.0f, cols), gb(global(a.gamma_b), 1.0f, cols),
-      bb(global(a.beta_b), 0.0f, cols), ga(global(a.gamma), 1.0f, cols),
-      be(global(a.beta), 0.0f, cols);
+  const Params<T, NC, ONE> gate(global(a.gate), 1.0f, cols, at),
+      gb(global(a.gamma_b), 1.0f, cols, at), bb(global(a.beta_b), 0.0f, cols, at),
+      ga(global(a.gamma), 1.0f, cols, at), be(global(a.beta), 0.0f, cols, at);
   const Share row = share_of(cols),
-              part = share_of(wave_cols<T, NC, W>((threadIdx.x >> 6) & (W - 1), cols));
+              part = share_of(at.part(at.wave, cols));
+  const int32_t other = (int32_t)threadIdx.x & 15;
+  const float n = other < at.waves ? (float)at.part(other, cols) : 0.0f;
   // the rows of a block go round together: its waves meet at the sums' barriers
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < rows; r0 += stride, r += stride) {
     const bool in = r < rows, more = r + stride < rows;
@@ -345,29 +405,30 @@ __global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_fwd(JoinFwd args
     if (!A && a.b && in) load(a.b, a.ldb, r, nb);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-      unpack_row<T>(in && a.b ? nb[c] : none, chunk_col<T, W>(c), cols, v[c]);
+      unpack_row<T>(in && a.b ? nb[c] : none, at.col(c), cols, v[c]);
     if (A && a.b && more) load(a.b, a.ldb, r + stride, nb);
     if (a.b) {
       if (a.gamma_b) {
-        const float rs = normalise<T, NC, W>(v, cols, a.kind, a.eta, row, part, lds, half);
+        const float rs = normalise(v, cols, at, a.kind, a.eta, row, part, n, lds, half);
         if (in && first_lane) global(a.rstd_b)[r] = rs;
       }
       if (a.qb && in) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) keep<T>(v[c], global(a.qb), global(a.eb), r, groups, chunk_col<T, W>(c));
+        for (int c = 0; c < NC; ++c)
+          keep<T>(v[c], global(a.qb), global(a.eb), r, groups, at.col(c));
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         float f[V], o[V];
         if (a.gamma_b) {
-          gb.get(c, cols, f);
-          bb.get(c, cols, o);
+          gb.get(c, at.col(c), cols, f);
+          bb.get(c, at.col(c), cols, o);
 #pragma unroll
           for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(v[c][j], f[j], o[j]);
         }
-        if (a.drop.threshold) drop<V>(a.drop, key, r, (cols + 7) / 8, chunk_col<T, W>(c), v[c]);
+        if (a.drop.threshold) drop<V>(a.drop, key, r, (cols + 7) / 8, at.col(c), v[c]);
         if (a.gate) {
-          gate.get(c, cols, f);
+          gate.get(c, at.col(c), cols, f);
 #pragma unroll
           for (int j = 0; j < V; ++j) v[c][j] *= f[j];
         }
@@ -378,28 +439,29 @@ __global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_fwd(JoinFwd args
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float x[V];
-      unpack_row<T>(in ? nx[c] : none, chunk_col<T, W>(c), cols, x);
+      unpack_row<T>(in ? nx[c] : none, at.col(c), cols, x);
 #pragma unroll
       for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(a.alpha, x[j], v[c][j]);
     }
     if (A && more) load(a.x, a.ldx, r + stride, nx);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int32_t col = chunk_col<T, W>(c);
-      if (a.r && in && col < cols) store_row(global(static_cast<T*>(a.r)) + r * a.ldr, col, cols, v[c]);
+      const int32_t col = at.col(c);
+      if (a.r && in && col < cols)
+        store_row(global(static_cast<T*>(a.r)) + r * a.ldr, col, cols, v[c]);
     }
     a = arguments(args);
     if (!a.gamma) continue;
-    const float rs = normalise<T, NC, W>(v, cols, a.kind, a.eta, row, part, lds, half);
+    const float rs = normalise(v, cols, at, a.kind, a.eta, row, part, n, lds, half);
     if (!in) continue;
     if (first_lane) global(a.rstd)[r] = rs;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int32_t col = chunk_col<T, W>(c);
+      const int32_t col = at.col(c);
       if (a.q) keep<T>(v[c], global(a.q), global(a.e), r, groups, col);
       float f[V], o[V];
-      ga.get(c, cols, f);
-      be.get(c, cols, o);
+      ga.get(c, at.col(c), cols, f);
+      be.get(c, at.col(c), cols, o);
 #pragma unroll
       for (int j = 0; j < V; ++j) v[c][j] = __builtin_fmaf(v[c][j], f[j], o[j]);
       if (col < cols) store_row(global(static_cast<T*>(a.z)) + r * a.ldz, col, cols, v[c]);
@@ -440,26 +502,28 @@ __device__ __forceinline__ void decode(bool there, lu2 q, uint32_t e, float (&v)
   for (int j = 0; j < kVec<T> / 4; ++j) dequant4(q[j], step, v + 4 * j);
 }
 
-template <typename T, int NC, int W>
-__device__ __forceinline__ void load_upper(const JoinBwd& a, int64_t r, BwdRow<NC>& w) {
+template <typename T, int NC, bool ONE>
+__device__ __forceinline__ void load_upper(const JoinBwd& a, const Where<T, NC, ONE>& at,
+                                           int64_t r, BwdRow<NC>& w) {
   if (!a.dz) return;
   const int32_t groups = (a.cols + kAct8Group - 1) / kAct8Group;
   w.rs = global(a.rstd)[r];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int32_t col = chunk_col<T, W>(c);
+    const int32_t col = at.col(c);
     w.dz[c] = load_raw(global(static_cast<const T*>(a.dz)) + r * a.lddz, col, a.cols);
     load_kept<T>(global(a.q), global(a.e), r, groups, col, a.cols, w.q[c], w.e[c]);
   }
 }
 
-template <typename T, int NC, int W>
-__device__ __forceinline__ void load_lower(const JoinBwd& a, int64_t r, BwdRow<NC>& w) {
+template <typename T, int NC, bool ONE>
+__device__ __forceinline__ void load_lower(const JoinBwd& a, const Where<T, NC, ONE>& at,
+                                           int64_t r, BwdRow<NC>& w) {
   const int32_t groups = (a.cols + kAct8Group - 1) / kAct8Group;
   if (a.gamma_b) w.rsb = global(a.rstd_b)[r];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int32_t col = chunk_col<T, W>(c);
+    const int32_t col = at.col(c);
     if (a.dr) w.dr[c] = load_raw(global(static_cast<const T*>(a.dr)) + r * a.lddr, col, a.cols);
     if (a.qb) load_kept<T>(global(a.qb), global(a.eb), r, groups, col, a.cols, w.qb[c], w.eb[c]);
   }
@@ -468,10 +532,10 @@ __device__ __forceinline__ void load_lower(const JoinBwd& a, int64_t r, BwdRow<N
 // The norm's input gradient from that of its normalised rows, in place.  What it
 // leaves past a row's end reaches no result: the sums of the branch there are not
 // stored, and the parameters, 0 there, keep it out of the next row sums.
-template <typename T, int NC, int W>
+template <typename T, int NC, bool ONE>
 __device__ __forceinline__ void through(float (&d)[NC][kVec<T>], const float (&h)[NC][kVec<T>],
-                                        float rs, int32_t cols, int kind,
-                                        float (*lds)[2][kThreads<W> / 64], int& half) {
+                                        float rs, const Share& row, const Where<T, NC, ONE>& at,
+                                        int kind, Meet<float> (*lds)[16], int& half) {
   constexpr int V = kVec<T>;
   float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
@@ -481,9 +545,16 @@ __device__ __forceinline__ void through(float (&d)[NC][kVec<T>], const float (&h
       s1 += d[c][j];
       s2 = __builtin_fmaf(d[c][j], h[c][j], s2);
     }
-  row_sums<W>(s1, s2, lds, half);
-  const float n = (float)cols;
-  const float m1 = kind == kNormLayer ? -rs * (s1 / n) : 0.0f, m2 = -s2 / n;
+  s1 = wave_total(s1);
+  s2 = wave_total(s2);
+  if constexpr (!ONE) {
+    const Meet<float> m = meet(s1, s2, at, lds, half);
+    s1 = sum16(((int32_t)threadIdx.x & 15) < at.waves ? m[0] : 0.0f);
+    s2 = sum16(m[1]);
+  }
+  const float n = (float)row.n, inv = (float)row.inv;
+  const float m1 = kind == kNormLayer ? -rs * quotient(s1, n, inv) : 0.0f;
+  const float m2 = -quotient(s2, n, inv);
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -491,51 +562,64 @@ __device__ __forceinline__ void through(float (&d)[NC][kVec<T>], const float (&h
       d[c][j] = __builtin_fmaf(__builtin_fmaf(m2, h[c][j], d[c][j]), rs, m1);
 }
 
-template <typename T, int NC, int W>
-__global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_bwd(JoinBwd args) {
+template <typename T, int NC, bool ONE>
+__global__ __launch_bounds__(1024, kWaves) void k_join_bwd(JoinBwd args) {
   JoinBwd a = arguments(args);
-  constexpr int V = kVec<T>, R = kRows<W>;
-  __shared__ float lds[2][2][kThreads<W> / 64];
+  constexpr int V = kVec<T>;
+  __shared__ Meet<float> lds[2][16];
   int half = 0;
   const int32_t cols = a.cols, worker = blockIdx.y;
+  const Where<T, NC, ONE> at(cols);
+  const int32_t R = block_rows<true>(at.waves);
   const int64_t rows = a.rows, base = worker * rows, stride = (int64_t)gridDim.x * R;
   const RngKey key = load_key(a.drop);
-  int64_t i = (int64_t)blockIdx.x * R + wave_row<W>();
+  int64_t i = (int64_t)blockIdx.x * R + at.row;
   constexpr bool A = kAhead<T, NC>;
   BwdRow<NC> next;
   if (A && i < rows) {
-    load_upper<T, NC, W>(a, base + i, next);
-    load_lower<T, NC, W>(a, base + i, next);
+    load_upper(a, at, base + i, next);
+    load_lower(a, at, base + i, next);
   }
-  const Params<T, NC, W> ga(global(a.gamma), 1.0f, cols), gate(global(a.gate), 1.0f, cols),
-      gb(global(a.gamma_b), 1.0f, cols);
-  float sums[4][NC][V];
+  const Params<T, NC, ONE> ga(global(a.gamma), 1.0f, cols, at),
+      gate(global(a.gate), 1.0f, cols, at), gb(global(a.gamma_b), 1.0f, cols, at);
+  const Share row = share_of(cols);
+  // At 16 columns a lane registers do not hold four sums (256 of 16384: 349 us, spilled,
+  // against 196): the branch's two lie in LDS, each lane's in its own place.
+  constexpr bool kLow = NC * V > 8;
+  constexpr int S = kLow ? 2 : 4;
+  using Low = float __attribute__((ext_vector_type(4)));
+  __shared__ Low low[kLow ? 2 : 1][kLow ? NC * V / 4 : 1][kLow ? 1024 : 1];
+  float sums[S][NC][V];
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
+  for (int s = 0; s < S; ++s)
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) sums[s][c][j] = 0.0f;
+  if constexpr (kLow) {
+    for (int s = 0; s < 2; ++s)
+      for (int i = 0; i < NC * V / 4; ++i) low[s][i][threadIdx.x] = Low{0.0f, 0.0f, 0.0f, 0.0f};
+  }
   for (int64_t i0 = (int64_t)blockIdx.x * R; i0 < rows; i0 += stride, i += stride) {
     const bool in = i < rows, more = i + stride < rows;
     const int64_t r = base + i;
     const lu4 none = {0u, 0u, 0u, 0u};
     float d[NC][V];
     a = arguments(args);
-    if (!A && in) load_upper<T, NC, W>(a, r, next);
+    if (!A && in) load_upper(a, at, r, next);
     if (a.dz) {
       float h[NC][V];
       const float rs = in ? next.rs : 0.0f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        unpack_row<T>(in ? next.dz[c] : none, chunk_col<T, W>(c), cols, d[c]);
+        unpack_row<T>(in ? next.dz[c] : none, at.col(c), cols, d[c]);
         decode<T>(in, next.q[c], next.e[c], h[c]);
       }
-      if (A && more) load_upper<T, NC, W>(a, r + stride, next);
+      if (A && more) load_upper(a, at, r + stride, next);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         float f[V];
-        ga.get(c, cols, f);
+        ga.get(c, at.col(c), cols, f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           sums[0][c][j] = __builtin_fmaf(d[c][j], h[c][j], sums[0][c][j]);
@@ -543,7 +627,7 @@ __global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_bwd(JoinBwd args
           d[c][j] *= f[j];
         }
       }
-      through<T, NC, W>(d, h, rs, cols, a.kind, lds, half);
+      through(d, h, rs, row, at, a.kind, lds, half);
     } else {
 #pragma unroll
       for (int c = 0; c < NC; ++c)
@@ -551,85 +635,114 @@ __global__ __launch_bounds__((kThreads<W>), kWaves) void k_join_bwd(JoinBwd args
         for (int j = 0; j < V; ++j) d[c][j] = 0.0f;
     }
     a = arguments(args);
-    if (!A && in) load_lower<T, NC, W>(a, r, next);
+    if (!A && in) load_lower(a, at, r, next);
     float k[NC][V];
     const float rsb = in ? next.rsb : 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       if (a.dr) {
         float o[V];
-        unpack_row<T>(in ? next.dr[c] : none, chunk_col<T, W>(c), cols, o);
+        unpack_row<T>(in ? next.dr[c] : none, at.col(c), cols, o);
 #pragma unroll
         for (int j = 0; j < V; ++j) d[c][j] += o[j];
       }
       decode<T>(in && a.qb, next.qb[c], next.eb[c], k[c]);
     }
-    if (A && more) load_lower<T, NC, W>(a, r + stride, next);
+    if (A && more) load_lower(a, at, r + stride, next);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int32_t col = chunk_col<T, W>(c);
+      const int32_t col = at.col(c);
       float o[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) o[j] = a.alpha * d[c][j];
       if (in && col < cols) store_row(global(static_cast<T*>(a.dx)) + r * a.lddx, col, cols, o);
       if (a.drop.threshold) drop<V>(a.drop, key, r, (cols + 7) / 8, col, d[c]);
+      if constexpr (kLow) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        sums[2][c][j] = __builtin_fmaf(d[c][j], k[c][j], sums[2][c][j]);
-        sums[3][c][j] += d[c][j];
+        for (int j = 0; j < V; j += 4) {
+          Low s = low[0][(c * V + j) / 4][threadIdx.x], t = low[1][(c * V + j) / 4][threadIdx.x];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[i] = __builtin_fmaf(d[c][j + i], k[c][j + i], s[i]);
+            t[i] += d[c][j + i];
+          }
+          low[0][(c * V + j) / 4][threadIdx.x] = s;
+          low[1][(c * V + j) / 4][threadIdx.x] = t;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          sums[2][c][j] = __builtin_fmaf(d[c][j], k[c][j], sums[2][c][j]);
+          sums[3][c][j] += d[c][j];
+        }
       }
       if (a.gate) {
-        gate.get(c, cols, o);
+        gate.get(c, at.col(c), cols, o);
 #pragma unroll
         for (int j = 0; j < V; ++j) d[c][j] *= o[j];
       }
       if (a.gamma_b) {
-        gb.get(c, cols, o);
+        gb.get(c, at.col(c), cols, o);
 #pragma unroll
         for (int j = 0; j < V; ++j) d[c][j] *= o[j];
       }
     }
     if (!a.db) continue;
-    if (a.gamma_b) through<T, NC, W>(d, k, rsb, cols, a.kind, lds, half);
+    if (a.gamma_b) through(d, k, rsb, row, at, a.kind, lds, half);
     if (!in) continue;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int32_t col = chunk_col<T, W>(c);
+      const int32_t col = at.col(c);
       if (col < cols) store_row(global(static_cast<T*>(a.db)) + r * a.lddb, col, cols, d[c]);
     }
   }
-  // the block's column sums: its rows add theirs in order
+  // the block's column sums: its rows' in order
   if (!a.part) return;
   float* part = global(a.part) + ((int64_t)worker * gridDim.x + blockIdx.x) * 4 * cols;
-  if constexpr (R > 1) {
-    __shared__ float all[4][NC * W * 64 * V];
-    for (int g = 0; g < R; ++g) {
-      if ((int)threadIdx.x / (W * 64) == g) {
+  if constexpr (!kLow) {
+    using Four4 = float __attribute__((ext_vector_type(4)));
+    __shared__ Four4 all[2][16 * kWaveCols<T, NC> / 4];
+    if (R > 1) {
+      const int32_t row_cols = at.waves * kWaveCols<T, NC>;
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < 4; s += 2) {  // the norm's two, then the branch's
+        if (s) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const int32_t at = chunk_col<T, W>(c) + j;
-              all[s][at] = (g ? all[s][at] : 0.0f) + sums[s][c][j];
+            for (int j = 0; j < V; j += 4) {
+              const float(&v)[V] = sums[s + t][c];
+              all[t][(at.row * row_cols + at.col(c) + j) / 4] =
+                  Four4{v[j], v[j + 1], v[j + 2], v[j + 3]};
             }
-      }
-      __syncthreads();
-    }
-    for (int32_t col = threadIdx.x; col < cols; col += kThreads<W>)
-      for (int s = 0; s < 4; ++s) part[s * cols + col] = all[s][col];
-  } else {
+        __syncthreads();
+        for (int32_t i = threadIdx.x; i < row_cols / 2; i += blockDim.x) {
+          const int32_t t = i / (row_cols / 4), four = i % (row_cols / 4);
+          Four4 v = all[t][four];
+          for (int32_t g = 1; g < R; ++g) v += all[t][g * (row_cols / 4) + four];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int32_t col = chunk_col<T, W>(c) + j;
-          if (col < cols) part[s * cols + col] = sums[s][c][j];
+          for (int j = 0; j < 4; ++j)
+            if (four * 4 + j < cols) part[(s + t) * cols + four * 4 + j] = v[j];
         }
+      }
+      return;
+    }
   }
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int32_t col = at.col(c) + j;
+        float v;
+        if constexpr (!kLow) v = sums[s][c][j];
+        else if (s < 2) v = sums[s & 1][c][j];
+        else v = low[s & 1][(c * V + j) / 4][threadIdx.x][j % 4];
+        if (col < cols) part[s * cols + col] = v;
+      }
 }
 
 // The parameters' gradients of a worker from its blocks' partial sums, in
@@ -676,43 +789,52 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_join_wgrad(JoinBwd a, int32
 }
 
 // ---- launchers -------------------------------------------------------------------
-// One round of resident blocks, and no more than there are rows for.
-constexpr int64_t kResident = 512;  // blocks of 512 threads, 4 waves a SIMD
+// One round of resident blocks, 16 waves to a CU, and no more than there are rows
+// for.
+constexpr int64_t kCus = 256, kCuWaves = 16;
 
-template <typename T, int NC, int W>
-void fwd(const JoinFwd& a, hipStream_t st) {
-  const int64_t want = (a.rows + kRows<W> - 1) / kRows<W>;
-  const int64_t most = kResident * 512 / kThreads<W>;
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_join_fwd<T, NC, W>), dim3((uint32_t)std::min(want, most)),
-                     dim3(kThreads<W>), 0, st, a);
-}
-
-template <typename T, int NC, int W>
-void bwd(const JoinBwd& a, hipStream_t st) {
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_join_bwd<T, NC, W>),
-                     dim3(join_bwd_blocks(a.n, a.rows, a.cols), a.n), dim3(kThreads<W>), 0, st, a);
+struct Shape {
+  int32_t waves, rows;  // to a row, and rows to a block
+  int64_t resident;
+};
+template <bool BACK>
+Shape shape_of(int32_t cols) {
+  const int32_t wave = cols <= 16 * 512 ? 512 : 1024;
+  Shape s;
+  s.waves = (cols + wave - 1) / wave;
+  s.rows = block_rows<BACK>(s.waves);
+  s.resident = kCus * (kCuWaves / (s.waves * s.rows));
+  return s;
 }
 
 // The instance that holds a row: 8 columns a lane, 16 above 8192 columns.
 // Binary32 rows take twice the pieces (M).
-template <typename T, class A, class F>
-void pick(const A& a, F&& f) {
+template <typename T, class F>
+void pick(int32_t cols, F&& f) {
   constexpr int M = 8 / kVec<T>;
-  if (a.cols <= 512) f(std::integral_constant<int, M>{}, std::integral_constant<int, 1>{});
-  else if (a.cols <= 1024) f(std::integral_constant<int, M>{}, std::integral_constant<int, 2>{});
-  else if (a.cols <= 2048) f(std::integral_constant<int, M>{}, std::integral_constant<int, 4>{});
-  else if (a.cols <= 4096) f(std::integral_constant<int, M>{}, std::integral_constant<int, 8>{});
-  else if (a.cols <= 8192) f(std::integral_constant<int, M>{}, std::integral_constant<int, 16>{});
-  else f(std::integral_constant<int, 2 * M>{}, std::integral_constant<int, 16>{});
+  if (cols <= 512) f(std::integral_constant<int, M>{}, std::true_type{});
+  else if (cols <= 16 * 512) f(std::integral_constant<int, M>{}, std::false_type{});
+  else f(std::integral_constant<int, 2 * M>{}, std::false_type{});
 }
 
 template <typename T>
 void fwd(const JoinFwd& a, hipStream_t st) {
-  pick<T>(a, [&](auto nc, auto w) { fwd<T, nc.value, w.value>(a, st); });
+  const Shape s = shape_of<false>(a.cols);
+  const int64_t blocks = std::min((a.rows + s.rows - 1) / s.rows, s.resident);
+  pick<T>(a.cols, [&](auto nc, auto one) {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_join_fwd<T, nc.value, one.value>), dim3((uint32_t)blocks),
+                       dim3(s.waves * s.rows * 64), 0, st, a);
+  });
 }
+
 template <typename T>
 void bwd(const JoinBwd& a, hipStream_t st) {
-  pick<T>(a, [&](auto nc, auto w) { bwd<T, nc.value, w.value>(a, st); });
+  const Shape s = shape_of<true>(a.cols);
+  pick<T>(a.cols, [&](auto nc, auto one) {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_join_bwd<T, nc.value, one.value>),
+                       dim3(join_bwd_blocks(a.n, a.rows, a.cols), a.n),
+                       dim3(s.waves * s.rows * 64), 0, st, a);
+  });
 }
 
 template <typename G>
@@ -725,10 +847,9 @@ void wgrad(const JoinBwd& a, hipStream_t st) {
 }  // namespace
 
 int32_t join_bwd_blocks(int32_t n, int64_t rows, int32_t cols) {
-  const int64_t per = cols <= 512 ? 8 : cols <= 1024 ? 4 : cols <= 2048 ? 2 : 1;
-  const int64_t all = cols <= 4096 ? kResident : kResident / 2;
-  const int64_t most = std::max<int64_t>(1, all / n);
-  return (int32_t)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, most));
+  const Shape s = shape_of<true>(cols);
+  const int64_t most = std::max<int64_t>(1, s.resident / n);
+  return (int32_t)std::max<int64_t>(1, std::min<int64_t>((rows + s.rows - 1) / s.rows, most));
 }
 
 void launch_join(const JoinFwd& a, hipStream_t st) {

@@ -40,6 +40,14 @@ __device__ __forceinline__ RngKey load_key(const Dropout& d) {
   return k;
 }
 
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+#else
+  return a ^ b ^ c;
+#endif
+}
+
 __device__ __forceinline__ lu4 philox(uint64_t block, uint32_t site, const RngKey& key) {
   uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = site, c3 = key.step;
   uint32_t k0 = key.k0, k1 = key.k1;
@@ -51,8 +59,8 @@ __device__ __forceinline__ lu4 philox(uint64_t block, uint32_t site, const RngKe
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c0 = xor3((uint32_t)(b >> 32), c1, k0);
+    c2 = xor3((uint32_t)(a >> 32), c3, k1);
     c1 = (uint32_t)b;
     c3 = (uint32_t)a;
     k0 += 0x9E3779B9u;
