@@ -603,11 +603,12 @@ class _Call:
     """Argument checks of one layer call: every tensor on the current device.
     Kept short: a small call's kernel takes 3 us, its launch as much."""
 
-    __slots__ = ("torch", "dev")
+    __slots__ = ("torch", "tensor", "dev")
 
     def __init__(self):
-        self.torch = _torch()
-        self.dev = self.torch.cuda.current_device()
+        self.torch = t = _torch()
+        self.tensor = t.Tensor
+        self.dev = t.cuda.current_device()
 
     def stream(self, stream):
         if stream is not None:
@@ -620,9 +621,11 @@ class _Call:
         return raw(self.dev) if raw else self.torch.cuda.current_stream(self.dev).cuda_stream
 
     def _on(self, t, name):
-        if not isinstance(t, self.torch.Tensor) or not t.is_cuda:
+        if not isinstance(t, self.tensor):
             raise TypeError(f"{name}: expected a CUDA tensor")
         if t.get_device() != self.dev:
+            if not t.is_cuda:
+                raise TypeError(f"{name}: expected a CUDA tensor")
             raise ValueError(f"{name}: on {t.device}, the current device is cuda:{self.dev}")
 
     def rows(self, t, name, rows=None, cols=None, dtype=None):
@@ -635,7 +638,8 @@ class _Call:
         r, c = shape
         if (rows is not None and r != rows) or (cols is not None and c != cols):
             raise ValueError(f"{name}: shape {tuple(t.shape)} != {(rows, cols)}")
-        if t.dtype not in _TYPES or (dtype is not None and t.dtype != dtype):
+        dt = t.dtype
+        if dt is not dtype and (dtype is not None or dt not in _TYPES):
             raise TypeError(f"{name}: dtype {t.dtype}" +
                             (f" != {dtype}" if dtype is not None else " not supported"))
         ld, one = t.stride()

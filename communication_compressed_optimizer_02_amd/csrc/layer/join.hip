@@ -848,8 +848,10 @@ void wgrad(const JoinBwd& a, hipStream_t st) {
 
 int32_t join_bwd_blocks(int32_t n, int64_t rows, int32_t cols) {
   const Shape s = shape_of<true>(cols);
-  const int64_t most = std::max<int64_t>(1, s.resident / n);
-  return (int32_t)std::max<int64_t>(1, std::min<int64_t>((rows + s.rows - 1) / s.rows, most));
+  const int64_t most = std::max<int64_t>(1, s.resident / n), want = (rows + s.rows - 1) / s.rows;
+  if (want <= most) return (int32_t)std::max<int64_t>(1, want);
+  const int64_t rounds = (want + most - 1) / most;  // no more blocks than these need
+  return (int32_t)((want + rounds - 1) / rounds);
 }
 
 void launch_join(const JoinFwd& a, hipStream_t st) {
