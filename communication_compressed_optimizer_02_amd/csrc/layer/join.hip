@@ -51,14 +51,14 @@ namespace {
 template <typename T, int NC>
 constexpr int32_t kWaveCols = NC * kVec<T> * 64;
 
-// Rows to a block: forward, eight of one wave, else one (its waves wait for no
+// Rows to a block: forward, four of one wave, else one (its waves wait for no
 // other row's).  Backward, where a block's rows share one partial sum, eight waves'
 // if they are whole rows, else what 16 waves hold: fewer partial sums, but all wait
 // for one another (1600 columns: 91 us against 100 with 16; 2500: 132 against 95,
 // 4096: 97 against 88, for 2^25 elements).
 template <bool BACK>
 __host__ __device__ inline int32_t block_rows(int32_t waves) {
-  if (!BACK) return waves == 1 ? 8 : 1;
+  if (!BACK) return waves == 1 ? 4 : 1;
   return waves == 1 || waves == 2 || waves == 4 ? 8 / waves : 16 / waves;
 }
 
@@ -789,21 +789,24 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_join_wgrad(JoinBwd a, int32
 }
 
 // ---- launchers -------------------------------------------------------------------
-// One round of resident blocks, 16 waves to a CU, and no more than there are rows
-// for.
-constexpr int64_t kCus = 256, kCuWaves = 16;
+// One round of resident blocks and no more than there are rows for: 16 waves to a
+// CU, which their registers allow; 20 forward of 16-bit rows, where blocks of up to
+// four waves fill the four SIMDs evenly (32768 x 1024 84 -> 79 us, 30203 x 1111 120 ->
+// 113; but 5 waves to a row 93 -> 116).
+constexpr int64_t kCus = 256, kCuWaves = 16, kCuWaves16 = 20;
 
 struct Shape {
   int32_t waves, rows;  // to a row, and rows to a block
   int64_t resident;
 };
 template <bool BACK>
-Shape shape_of(int32_t cols) {
+Shape shape_of(int32_t cols, bool two_bytes = false) {
   const int32_t wave = cols <= 16 * 512 ? 512 : 1024;
   Shape s;
   s.waves = (cols + wave - 1) / wave;
   s.rows = block_rows<BACK>(s.waves);
-  s.resident = kCus * (kCuWaves / (s.waves * s.rows));
+  const int64_t all = !BACK && two_bytes && s.waves <= 4 ? kCuWaves16 : kCuWaves;
+  s.resident = kCus * (all / (s.waves * s.rows));
   return s;
 }
 
@@ -819,7 +822,7 @@ void pick(int32_t cols, F&& f) {
 
 template <typename T>
 void fwd(const JoinFwd& a, hipStream_t st) {
-  const Shape s = shape_of<false>(a.cols);
+  const Shape s = shape_of<false>(a.cols, sizeof(T) == 2);
   const int64_t blocks = std::min((a.rows + s.rows - 1) / s.rows, s.resident);
   pick<T>(a.cols, [&](auto nc, auto one) {
     hipLaunchKernelGGL(HIP_KERNEL_NAME(k_join_fwd<T, nc.value, one.value>), dim3((uint32_t)blocks),
