@@ -264,7 +264,8 @@ __device__ __forceinline__ float normalise(float (&v)[NC][kVec<T>], int32_t cols
     squares = (double)s2;
     if constexpr (!ONE) squares = (double)sum16((float)meet(0.0, squares, at, lds, half)[1]);
   }
-  const float rs = inv_root((float)(squares * row.inv) + eta);
+  // the squares around the mean are a difference and, for equal values, may be less than 0
+  const float var = (float)(squares * row.inv), rs = inv_root((var < 0.0f ? 0.0f : var) + eta);
   if (kind == kNormLayer) {
     const float low = -off * rs;
 #pragma unroll

@@ -77,7 +77,8 @@ int oba_residual_norm(int64_t rows, int64_t cols, int dtype, int kind, double et
                       int8_t* q, uint8_t* e, hipStream_t stream) {
   oba::Dropout d;
   if (!is_type(dtype) || !kind_ok(kind) || !sizes_ok(rows, cols, oba::kMaxNormCols) ||
-      !std::isfinite(eta) || eta < 0.0 || !std::isfinite(alpha) || !ld_ok(ldx, cols) ||
+      !std::isfinite((float)eta) || eta < 0.0 || !std::isfinite((float)alpha) ||
+      !ld_ok(ldx, cols) ||
       (b && !ld_ok(ldb, cols)) || (r && !ld_ok(ldr, cols)) || (gamma && !ld_ok(ldz, cols)) ||
       !make_dropout(rate, rng, site, d))
     return OBA_EINVAL;
@@ -128,7 +129,7 @@ int oba_residual_norm_backward(int32_t n, int64_t rows, int64_t cols, int dtype,
                                size_t ws_bytes, hipStream_t stream) {
   oba::Dropout d;
   if (!is_type(dtype) || !is_type(g_dtype) || !kind_ok(kind) || !workers_ok(n, rows) ||
-      !sizes_ok(n * rows, cols, oba::kMaxNormCols) || !std::isfinite(alpha) ||
+      !sizes_ok(n * rows, cols, oba::kMaxNormCols) || !std::isfinite((float)alpha) ||
       !ld_ok(lddx, cols) || (gamma && !ld_ok(lddz, cols)) || (dr && !ld_ok(lddr, cols)) ||
       (db && !ld_ok(lddb, cols)) || !make_dropout(rate, rng, site, d))
     return OBA_EINVAL;

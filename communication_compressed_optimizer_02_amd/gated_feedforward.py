@@ -15,9 +15,10 @@ gradients of the n workers go to the same range of its gradient rows g, and what
 the backward pass needs is kept in 8 bits: the normalised rows, both products'
 inputs, both pre-activations, and norm_b's rows (with post or scale).  Dropout
 keeps no mask: its rows' bits come from rng = {seed, step} on the device, so add
-1 to rng[1] after each step (in a captured step too).  An element's bits depend
-on its row, its column and its sub-layer.  The rows of the workers follow each
-other: worker i's are [i*rows, (i+1)*rows).
+1 to rng[1] after each step (in a captured step too).  An element's bits depend on
+its row, its column and its sub-layer's number, counted from `site`: instances of
+one seed that run in one step have sites of their own.  The rows of the workers
+follow each other: worker i's are [i*rows, (i+1)*rows).
 
     F = GatedFeedForward(width, hidden, n, rows, layers=4, rate=0.1, seed=1)
     L = Layout(F.size, n, ...); S = State(L, "bf16")
@@ -41,8 +42,8 @@ from . import binding as oba
 
 class GatedFeedForward:
     def __init__(self, width, hidden, n, rows, layers=1, dtype="bf16", gate="silu", norm="rms",
-                 eta=1e-5, alpha=1.0, rate=0.0, seed=0, post=False, scale=False, at=0,
-                 share=None):
+                 eta=1e-5, alpha=1.0, rate=0.0, seed=0, site=0, post=False, scale=False,
+                 at=0, share=None):
         import torch
 
         if gate not in oba.GATES:
@@ -58,7 +59,7 @@ class GatedFeedForward:
         self.sizes = sizes
         self.width, self.hidden, self.n, self.rows, self.layers = width, hidden, n, rows, layers
         self.gate, self.norm, self.eta, self.alpha, self.rate = gate, norm, eta, alpha, rate
-        self.post, self.scale = post, scale
+        self.site, self.post, self.scale = site, post, scale
         self.flat = None  # the parameters that load() was given
         self.kept = False  # whether a forward() has left what backward() reads
         self.dtype = sizes[4]
@@ -148,7 +149,7 @@ class GatedFeedForward:
         """Sub-layer `layer`'s sum's parameters."""
         return dict(alpha=self.alpha, gate=self._opt(layer, "scale"),
                     gamma_b=self._opt(layer, "gamma_b"), beta_b=self._opt(layer, "beta_b"),
-                    site=layer)
+                    site=self.site + layer)
 
     def _next(self, layer, z, keep, m):
         """The norm of sub-layer `layer`."""

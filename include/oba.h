@@ -529,11 +529,11 @@ enum { OBA_NORM_LAYER = 0, OBA_NORM_RMS = 1 };
  *   r = alpha * x + gate * dropout(n)        (b NULL: r = alpha * x)
  *   z = norm(r) * gamma + beta               (gamma NULL: none)
  * x, b, r, z: rows of one dtype, at most 2^14 columns; z comes from r before it
- * is rounded.  gate, beta_b, beta: or NULL (1, 0, 0).  r: or NULL if gamma is
- * given.  rstd_b, rstd: [rows] binary32 out, with gamma_b and with gamma.  qb,
- * eb: NULL, or norm(b) (b itself without gamma_b) kept in 8 bits; q, e: NULL, or
- * norm(r).  Without b none of its arguments may be given, and without gamma_b or
- * gamma none of theirs. */
+ * is rounded.  eta (not below 0) and alpha are finite in binary32.  gate, beta_b,
+ * beta: or NULL (1, 0, 0).  r: or NULL if gamma is given.  rstd_b, rstd: [rows]
+ * binary32 out, with gamma_b and with gamma.  qb, eb: NULL, or norm(b) (b itself
+ * without gamma_b) kept in 8 bits; q, e: NULL, or norm(r).  Without b none of its
+ * arguments may be given, and without gamma_b or gamma none of theirs. */
 int oba_residual_norm(int64_t rows, int64_t cols, int dtype, int kind, double eta, const void* x,
                       int64_t ldx, double alpha, const void* b, int64_t ldb, const float* gamma_b,
                       const float* beta_b, const float* gate, double rate, const uint64_t* rng,

@@ -65,7 +65,7 @@ def params64(F, flat):
     return out
 
 
-FORMS = [dict(layers=1), dict(layers=2, norm="layer", gate="gelu", rate=0.3, alpha=0.5),
+FORMS = [dict(layers=1), dict(layers=2, norm="layer", gate="gelu", rate=0.3, alpha=0.5, site=9),
          dict(layers=3, rate=0.1, post=True, scale=True, dtype="f16"),
          dict(layers=2, norm="layer", post=True, gate="sigmoid"),
          dict(layers=2, scale=True, gate="gelu_tanh", rate=0.2, dtype="f16")]
@@ -95,7 +95,7 @@ def test_a_pass_against_the_model(width, hidden, n, r, form):
     dx = F.backward(dy, S.g)
     t.cuda.synchronize()
     seed, step = (int(v) for v in F.rng.cpu())
-    masks = [factor_gpu(n * r, width, F.rate, seed, step, k) for k in range(F.layers)]
+    masks = [factor_gpu(n * r, width, F.rate, seed, step, F.site + k) for k in range(F.layers)]
     p = params64(F, S.x)
     xx = x.double().requires_grad_(True)
     assert off(y, model64(F, xx.detach(), p, masks)) <= 0.04
@@ -171,7 +171,8 @@ def by_one(F, x, dy, flat, g):
             norms.append((qn, rn))
         oba.residual_norm(r, F.eta, b=b, alpha=F.alpha, gate=P(k, "scale"),
                           gamma_b=P(k, "gamma_b"), beta_b=P(k, "beta_b"), rstd_b=rb, qb=kb[0],
-                          eb=kb[1], rate=F.rate, rng=F.rng, site=k, r=out, kind=F.norm, **nxt)
+                          eb=kb[1], rate=F.rate, rng=F.rng, site=F.site + k, r=out, kind=F.norm,
+                          **nxt)
         r = out
         keep.append((kz, kp, ku, kh, kb, rb))
     dz, dr = None, dy
@@ -190,7 +191,7 @@ def by_one(F, x, dy, flat, g):
             a.update(alpha=F.alpha, db=db, qb=kb[0], eb=kb[1], rstd_b=rb, gamma_b=P(k, "gamma_b"),
                      beta_b=P(k, "beta_b"), gate=P(k, "scale"), at_gate=at(k, "scale"),
                      at_gamma_b=at(k, "gamma_b"), at_beta_b=at(k, "beta_b"), rate=F.rate,
-                     rng=F.rng, site=k)
+                     rng=F.rng, site=F.site + k)
         oba.residual_norm_backward(n, dx, g, wsb, dr=dr, kind=F.norm, **a)
         dr = dx
         if k < 0:

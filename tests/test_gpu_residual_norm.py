@@ -176,6 +176,24 @@ def test_rows_far_from_zero_and_constant_rows(c):
     assert bool((o["r"][0][3:5] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("c", [500, 777, 1600, 5000, 9001])
+def test_large_constant_rows_stay_finite(c, dtype):
+    """A row of one large value of 24 bits: its squares around the mean are a difference of equal
+    sums and may not become less than 0.  Its centred values are what the mean is off
+    by, at most 20 units of the first sum's error of 20 units, over sqrt(eta)."""
+    t = torch()
+    vals = 10 ** (t.rand(300, generator=gen(c), device="cuda") * (2 if dtype == "f16" else 13) + 2)
+    buf = t.zeros((300, (c + 7) // 8 * 8), device="cuda", dtype=dt(dtype))
+    buf[:, :c] = vals[:, None].to(dt(dtype))
+    z, rstd = t.empty_like(buf)[:, :c], t.zeros(300, device="cuda")
+    oba.residual_norm(buf[:, :c], ETA, alpha=1.1, gamma=t.ones(c, device="cuda"), z=z, rstd=rstd)
+    t.cuda.synchronize()
+    assert bool(t.isfinite(z).all()) and bool((rstd > 0).all())
+    off = 0 if dtype == "f32" else 440 * UNIT * UNIT * buf[:, :1].double() / ETA ** 0.5
+    assert bool((z.double().abs() <= off * (1 + 2 ** -7)).all())
+
+
 def test_infinities_and_nan_stay_in_their_rows():
     t = torch()
     for kind in ("layer", "rms"):

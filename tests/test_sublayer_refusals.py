@@ -67,6 +67,7 @@ CASES = {
         (dict(ldz=8), EINVAL), (dict(dtype=3), EINVAL), (dict(kind=2), EINVAL),
         (dict(kind=-1), EINVAL), (dict(eta=-1.0), EINVAL), (dict(eta=NAN), EINVAL),
         (dict(alpha=INF), EINVAL), (dict(alpha=NAN), EINVAL), (dict(rate=1.0), EINVAL),
+        (dict(alpha=1e39), EINVAL), (dict(eta=1e39), EINVAL),
         (dict(rate=-1e-9), EINVAL), (dict(x=None), EINVAL), (dict(x=A + 8), EALIGN),
         (dict(b=None), EINVAL), (dict(b=A + 8), EALIGN), (dict(gamma_b=None), EINVAL),
         (dict(gamma_b=None, beta_b=None), EINVAL), (dict(rstd_b=None), EINVAL),
@@ -81,6 +82,7 @@ CASES = {
     + [(dict(NO_BRANCH, rate=0.1, rng=A), EINVAL)]
     + [(dict({**NO_NORM, k: A}), EINVAL) for k in ("beta", "z", "rstd", "q", "e")],
     "oba_residual_norm_backward": [
+        (dict(alpha=-1e39), EINVAL),
         (dict(n=0), EINVAL), (dict(n=4097), EINVAL), (dict(rows=-1), EINVAL),
         (dict(rows=1 << 30), EINVAL), (dict(cols=0), EINVAL), (dict(cols=16385), EINVAL),
         (dict(dtype=3), EINVAL), (dict(g_dtype=-1), EINVAL), (dict(kind=2), EINVAL),
