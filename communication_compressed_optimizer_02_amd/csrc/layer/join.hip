@@ -699,9 +699,10 @@ __global__ __launch_bounds__(1024, kWaves) void k_join_bwd(JoinBwd args) {
   }
   // the block's column sums: its rows' in order
   if (!a.part) return;
-  float* part = global(a.part) + ((int64_t)worker * gridDim.x + blockIdx.x) * 4 * cols;
+  using Four4 = float __attribute__((ext_vector_type(4)));
+  const int64_t pc = join_part_cols(cols);
+  float* part = global(a.part) + ((int64_t)worker * gridDim.x + blockIdx.x) * 4 * pc;
   if constexpr (!kLow) {
-    using Four4 = float __attribute__((ext_vector_type(4)));
     __shared__ Four4 all[2][16 * kWaveCols<T, NC> / 4];
     if (R > 1) {
       const int32_t row_cols = at.waves * kWaveCols<T, NC>;
@@ -723,9 +724,7 @@ __global__ __launch_bounds__(1024, kWaves) void k_join_bwd(JoinBwd args) {
           const int32_t t = i / (row_cols / 4), four = i % (row_cols / 4);
           Four4 v = all[t][four];
           for (int32_t g = 1; g < R; ++g) v += all[t][g * (row_cols / 4) + four];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (four * 4 + j < cols) part[(s + t) * cols + four * 4 + j] = v[j];
+          if (four * 4 < cols) *reinterpret_cast<Four4*>(part + (s + t) * pc + four * 4) = v;
         }
       }
       return;
@@ -736,13 +735,16 @@ __global__ __launch_bounds__(1024, kWaves) void k_join_bwd(JoinBwd args) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
+      for (int j = 0; j < V; j += 4) {
+        Four4 v;
+        if (kLow && s >= 2) {
+          v = low[s & 1][kLow ? (c * V + j) / 4 : 0][kLow ? threadIdx.x : 0];
+        } else {
+          const float(&w)[V] = sums[kLow ? s & 1 : s][c];
+          v = Four4{w[j], w[j + 1], w[j + 2], w[j + 3]};
+        }
         const int32_t col = at.col(c) + j;
-        float v;
-        if constexpr (!kLow) v = sums[s][c][j];
-        else if (s < 2) v = sums[s & 1][c][j];
-        else v = low[s & 1][(c * V + j) / 4][threadIdx.x][j % 4];
-        if (col < cols) part[s * cols + col] = v;
+        if (col < cols) *reinterpret_cast<Four4*>(part + s * pc + col) = v;
       }
 }
 
@@ -755,14 +757,14 @@ template <typename G>
 __global__ __launch_bounds__(kJoinWaves * 64) void k_join_wgrad(JoinBwd a, int32_t blocks) {
   __shared__ double lds[kJoinWaves][2][64];
   const int32_t l = threadIdx.x & 63, w = threadIdx.x >> 6, col = blockIdx.x * 64 + l;
-  const int64_t cols = a.cols, worker = blockIdx.y;
-  const float* p = a.part + (worker * blocks * 4 + blockIdx.z * 2) * cols + col;
+  const int64_t cols = a.cols, pc = join_part_cols(cols), worker = blockIdx.y;
+  const float* p = a.part + (worker * blocks * 4 + blockIdx.z * 2) * pc + col;
   double s = 0.0, t = 0.0;
   if (col < cols) {
 #pragma unroll 4
     for (int32_t b = w; b < blocks; b += kJoinWaves) {
-      s += p[(int64_t)b * 4 * cols];
-      t += p[((int64_t)b * 4 + 1) * cols];
+      s += p[(int64_t)b * 4 * pc];
+      t += p[((int64_t)b * 4 + 1) * pc];
     }
   }
   lds[w][0][l] = s;

@@ -30,7 +30,8 @@ bool kind_ok(int kind) { return kind == OBA_NORM_LAYER || kind == OBA_NORM_RMS; 
 int check_opt(const void* p, uintptr_t align) { return p ? check_ptr(p, align) : OBA_OK; }
 
 size_t join_ws(int32_t n, int64_t rows, int64_t cols) {
-  return (size_t)n * oba::join_bwd_blocks(n, rows, (int32_t)cols) * 4 * cols * sizeof(float);
+  return (size_t)n * oba::join_bwd_blocks(n, rows, (int32_t)cols) * 4 * oba::join_part_cols(cols) *
+         sizeof(float);
 }
 
 bool gated_ok(GatedKind kind, int dtype, int gate, int64_t rows, int64_t hidden, int64_t k) {

@@ -82,6 +82,8 @@ struct JoinBwd {
 };
 // Blocks of the backward pass per worker.
 int32_t join_bwd_blocks(int32_t n, int64_t rows, int32_t cols);
+// columns of a partial sum: whole 16 bytes
+__host__ __device__ inline int64_t join_part_cols(int64_t cols) { return (cols + 3) / 4 * 4; }
 void launch_join_backward(const JoinBwd& a, hipStream_t st);
 void launch_join_weight_grad(const JoinBwd& a, hipStream_t st);
 
