@@ -109,14 +109,26 @@ class GatedFeedForward:
         self.r = [matrix(total, width) for _ in range(2)]  # r, and its gradients
         self.spare = [torch.empty(total, device="cuda") for _ in range(2)]  # infer()'s rstd
         self.dpu, self.dz, self.db = (matrix(total, c) for c in (2 * hidden, width, width))
-        self.ws = max((oba.gated_linear_workspace(total, width, hidden),
-                       oba.linear_workspace(total, hidden, width),
+        self.ws = max((self._infer_workspace(total),
                        oba.gated_hidden_grad_workspace(total, hidden, width),
                        oba.linear_workspace(total, width, 2 * hidden),
                        oba.linear_weight_grad_workspace(n, rows, width, 2 * hidden),
                        oba.linear_weight_grad_workspace(n, rows, hidden, width),
                        oba.residual_norm_backward_workspace(n, rows, width)),
                       key=lambda t: t.numel())
+
+    def _infer_workspace(self, total):
+        """For every number of rows up to total: products of few tiles split their
+        sums, so that fewer rows may need more.  Tiles are 64 or 128 rows high: of the
+        counts between two multiples of 64 the last needs the most, and above 2^14 rows
+        no product has so few tiles."""
+        c = oba.lib()
+        counts = {min(m, total) for m in range(64, min(total, 1 << 14) + 64, 64)} | {total}
+        at = max(counts, key=lambda m: max(
+            c.oba_gated_linear_workspace_bytes(m, self.width, self.hidden),
+            c.oba_linear_workspace_bytes(m, self.hidden, self.width)))
+        return max((oba.gated_linear_workspace(at, self.width, self.hidden),
+                    oba.linear_workspace(at, self.hidden, self.width)), key=lambda t: t.numel())
 
     def part(self, flat, layer, name):
         """A parameter's slice of the flat vector (or of a row of g)."""

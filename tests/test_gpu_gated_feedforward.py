@@ -249,6 +249,21 @@ def test_inference_drops_nothing_and_keeps_what_forward_kept():
     LE.close()
 
 
+@pytest.mark.parametrize("width,hidden,n,r", [(1024, 4096, 8, 2048), (4096, 1024, 16, 320),
+                                              (1600, 6400, 8, 256)])
+def test_inference_of_any_number_of_rows(width, hidden, n, r):
+    """Fewer rows may need more workspace than all: their products' sums are split."""
+    t = torch()
+    say(f"[gff] infer rows {width} {hidden}")
+    F, L, S, x, _ = make(width, hidden, n, r, 7)
+    want = F.infer(x).clone()
+    for m in (1, 33, 64, 65, 100, 127, 128, 129, 255, 257, 300, 511, 700, 1025, n * r - 1):
+        y = F.infer(x[:m])
+        t.cuda.synchronize()
+        assert off(y, want[:m].double()) <= 0.04, m  # roundings, as above
+    L.close()
+
+
 def test_instances_that_share_scratch():
     t = torch()
     say("[gff] share")
