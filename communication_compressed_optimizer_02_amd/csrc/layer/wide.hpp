@@ -68,7 +68,7 @@ struct AheadStage {
   // Pieces first .. first + n - 1 of a whole step straight to LDS, without a wait.
   // Five wait states lie between a vector instruction's write of a scalar register
   // (the buffer's) and a load that reads it, one between the write of m0 and the
-  // load; nothing else in these kernels uses m0.
+  // load.  m0, which the compiler does not take as clobbered, is left as it was.
   __device__ __forceinline__ void ahead(int wave, const char* base, char* lds, int first = 0,
                                         int n = P) const {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -81,11 +81,15 @@ struct AheadStage {
     const uint32_t to = (uint32_t)(uintptr_t)(lp)lds + wave * 1024u;
 #pragma unroll
     for (int p = 0; p < P; ++p)
-      if (p >= first && p < first + n)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     :
-                     : "s"(to + p * NT * 16), "v"(off[p]), "s"(r)
-                     : "memory");
+      if (p >= first && p < first + n) {
+        int m0;
+        asm volatile(
+            "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 2\n\t"
+            "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+            : "=&s"(m0)
+            : "s"(to + p * NT * 16), "v"(off[p]), "s"(r)
+            : "memory");
+      }
 #endif
   }
 
