@@ -40,6 +40,26 @@ from __future__ import annotations
 from . import binding as oba
 
 
+# Products of few tiles split their sums and need a workspace: gated ones of at most 128
+# tiles of 64 rows, linear ones of at most 256 tiles of 128 rows.
+_SPLIT_ROWS = 256 * 128
+
+
+def _product_bytes(rows, width, hidden):
+    """The workspace of a forward pass's products for so many rows."""
+    c = oba.lib()
+    return max(c.oba_gated_linear_workspace_bytes(rows, width, hidden),
+               c.oba_linear_workspace_bytes(rows, hidden, width))
+
+
+def _hungriest(width, hidden, total):
+    """The number of rows up to total whose products need the largest workspace: fewer
+    rows, split more often, may need more.  Of the counts between two multiples of 64,
+    whose tiles are the same, the last needs the most."""
+    counts = {min(m, total) for m in range(64, min(total, _SPLIT_ROWS) + 64, 64)} | {total}
+    return max(counts, key=lambda m: _product_bytes(m, width, hidden))
+
+
 class GatedFeedForward:
     def __init__(self, width, hidden, n, rows, layers=1, dtype="bf16", gate="silu", norm="rms",
                  eta=1e-5, alpha=1.0, rate=0.0, seed=0, site=0, post=False, scale=False,
@@ -118,15 +138,8 @@ class GatedFeedForward:
                       key=lambda t: t.numel())
 
     def _infer_workspace(self, total):
-        """For every number of rows up to total: products of few tiles split their
-        sums, so that fewer rows may need more.  Tiles are 64 or 128 rows high: of the
-        counts between two multiples of 64 the last needs the most, and above 2^14 rows
-        no product has so few tiles."""
-        c = oba.lib()
-        counts = {min(m, total) for m in range(64, min(total, 1 << 14) + 64, 64)} | {total}
-        at = max(counts, key=lambda m: max(
-            c.oba_gated_linear_workspace_bytes(m, self.width, self.hidden),
-            c.oba_linear_workspace_bytes(m, self.hidden, self.width)))
+        """For every number of rows up to total."""
+        at = _hungriest(self.width, self.hidden, total)
         return max((oba.gated_linear_workspace(at, self.width, self.hidden),
                     oba.linear_workspace(at, self.hidden, self.width)), key=lambda t: t.numel())
 
