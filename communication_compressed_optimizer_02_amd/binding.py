@@ -867,9 +867,13 @@ def linear_weight_grad(n, dy, q, e, g, n_in, at_w, at_bias, ws, stream=None):
 
 def dropout_rng(seed, step=0):
     """The device's {seed, step} that dropout and residual_norm read: int64 [2].
-    A training step ends with rng[1] += 1, also inside a captured one."""
+    seed: any 64 bits, as a number with or without a sign.  A training step ends with
+    rng[1] += 1, also inside a captured one."""
     import torch
 
+    if not -(1 << 63) <= seed < 1 << 64:
+        raise ValueError(f"seed: {seed} has more than 64 bits")
+    seed = seed - (1 << 64) if seed >= 1 << 63 else seed
     return torch.tensor([seed, step], dtype=torch.int64, device="cuda")
 
 
