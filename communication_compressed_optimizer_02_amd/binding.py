@@ -599,6 +599,13 @@ def _torch():
     return _torch_module
 
 
+def _named(table, name, what):
+    """The number of a kind that goes by its name."""
+    if name not in table:
+        raise ValueError(f"{what}: {name!r} is none of {sorted(table)}")
+    return table[name]
+
+
 class _Call:
     """Argument checks of one layer call: every tensor on the current device.
     Kept short: a small call's kernel takes 3 us, its launch as much."""
@@ -908,7 +915,7 @@ def residual_norm(x, eta, b=None, alpha=1.0, gate=None, gamma_b=None, beta_b=Non
     qbp, ebp = c.kept(qb, eb, rows, cols)
     qp, ep = c.kept(q, e, rows, cols)
     _check(lib().oba_residual_norm(
-        rows, cols, _TYPES[dt], NORMS[kind], eta, xp, ldx, alpha, bp, ldb,
+        rows, cols, _TYPES[dt], _named(NORMS, kind, "kind"), eta, xp, ldx, alpha, bp, ldb,
         c.opt(gamma_b, "gamma_b", cols), c.opt(beta_b, "beta_b", cols), c.opt(gate, "gate", cols),
         rate, c.rng(rng), site, c.opt(rstd_b, "rstd_b", rows), qbp, ebp, rp, ldr,
         c.opt(gamma, "gamma", cols), c.opt(beta, "beta", cols), zp, ldz,
@@ -946,7 +953,7 @@ def residual_norm_backward(n, dx, g, ws, dz=None, dr=None, alpha=1.0, q=None, e=
         gt, ldg, gp = c.grads(g, n, *((at, cols) for at in places))
     wp, wb = c.ws(ws)
     _check(lib().oba_residual_norm_backward(
-        n, total // n, cols, _TYPES[dt], NORMS[kind], dzp, lddz, qp, ep,
+        n, total // n, cols, _TYPES[dt], _named(NORMS, kind, "kind"), dzp, lddz, qp, ep,
         c.opt(rstd, "rstd", total), c.opt(gamma, "gamma", cols), drp, lddr, alpha, dxp, lddx,
         qbp, ebp, c.opt(rstd_b, "rstd_b", total), c.opt(gamma_b, "gamma_b", cols),
         c.opt(beta_b, "beta_b", cols), c.opt(gate, "gate", cols), rate, c.rng(rng), site,
@@ -974,7 +981,7 @@ def gated_linear(x, w, y, ws, bias=None, gate="silu", qp=None, ep=None, qu=None,
     sp, sb = c.ws(ws)
     _check(lib().oba_gated_linear(
         rows, n_in, hidden, xp, ldx, wp, ldw, _TYPES[x.dtype], c.opt(bias, "bias", 2 * hidden),
-        GATES[gate], yp, ldy, *kept, sp, sb, c.stream(stream)), "oba_gated_linear")
+        _named(GATES, gate, "gate"), yp, ldy, *kept, sp, sb, c.stream(stream)), "oba_gated_linear")
 
 
 def gated_hidden_grad_workspace(rows, hidden, n_out):
@@ -997,8 +1004,8 @@ def gated_hidden_grad(dy, w, qp, ep, qu, eu, dpu, ws, gate="silu", stream=None):
     kept = (*c.kept(qp, ep, rows, hidden), *c.kept(qu, eu, rows, hidden))
     sp, sb = c.ws(ws)
     _check(lib().oba_gated_hidden_grad(
-        rows, hidden, n_out, dyp, lddy, wp, ldw, _TYPES[dy.dtype], GATES[gate], *kept, dp, ldd, sp,
-        sb, c.stream(stream)), "oba_gated_hidden_grad")
+        rows, hidden, n_out, dyp, lddy, wp, ldw, _TYPES[dy.dtype], _named(GATES, gate, "gate"),
+        *kept, dp, ldd, sp, sb, c.stream(stream)), "oba_gated_hidden_grad")
 
 
 def timing_enable(on=True, capacity=4096):

@@ -72,8 +72,10 @@ class GatedFeedForward:
             raise ValueError(f"norm: {norm!r} is none of {sorted(oba.NORMS)}")
         if layers < 1:
             raise ValueError(f"layers: {layers}")
-        sizes = (width, hidden, n, rows, {"f16": torch.float16, "bf16": torch.bfloat16}[dtype],
-                 torch.cuda.current_device())
+        types = {"f16": torch.float16, "bf16": torch.bfloat16}
+        if dtype not in types:
+            raise ValueError(f"dtype: {dtype!r} is none of {sorted(types)}")
+        sizes = (width, hidden, n, rows, types[dtype], torch.cuda.current_device())
         if share is not None and share.sizes != sizes:
             raise ValueError(f"share: an instance of {share.sizes}, not of {sizes}")
         self.sizes = sizes
