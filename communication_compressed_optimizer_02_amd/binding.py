@@ -902,9 +902,10 @@ def residual_norm(x, eta, b=None, alpha=1.0, gate=None, gamma_b=None, beta_b=Non
                   z=None, rstd=None, q=None, e=None, kind="layer", stream=None):
     """r = alpha x + gate * dropout(norm(b) * gamma_b + beta_b) and
     z = norm(r) * gamma + beta, kind "layer" or "rms".  Without gamma_b no norm of
-    b, without gamma none of r; r or z may be left out.  With (qb, eb) norm(b)
-    (or b) is kept in 8 bits, with (q, e) norm(r); rstd_b and rstd [rows] float32
-    are written."""
+    b, without gamma none of r (then no z and no rstd); with it r may be left out.
+    With (qb, eb) norm(b) (or b) is kept in 8 bits, with (q, e) norm(r).  rstd_b and
+    rstd [rows] float32 are written, and belong to their norm whether it is kept or
+    not."""
     c = _Call()
     xp, ldx = c.rows(x, "x")
     rows, cols = x.shape
