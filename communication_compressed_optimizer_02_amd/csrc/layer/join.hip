@@ -28,9 +28,10 @@
 // of the unit's time at 32768 x 1024.  So waves without columns are what costs most:
 // with the waves a row rounded up to 1, 2, 4, 8 or 16, 33.5 million bfloat16 elements
 // of 2500 columns took 157 us, of 4500 199 us, and 93 and 136 with the waves counted
-// out.  Measured, both norms, dropout, all kept, bfloat16: 32768 x 1024 80 us (4.2
-// TB/s), 8192 x 4096 81 us (4.2 TB/s), back 79 and 87 us; binary32, the RMS norm of
-// 2048 x 8192 58 us (5.0 TB/s).
+// out; a row narrower than a wave takes a wave all the same (256 columns 121 us, 64 437).
+// Measured, both norms, dropout, all kept, bfloat16: 32768 x 1024 80 us (4.2 TB/s), 8192 x
+// 4096 82 us (4.1 TB/s), back 79 and 88 us; binary32, the RMS norm of 2048 x 8192 58 us
+// (5.0 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -600,7 +601,7 @@ __global__ __launch_bounds__(1024, kWaves) void k_join_bwd(JoinBwd args) {
       gate(global(a.gate), 1.0f, cols, at), gb(global(a.gamma_b), 1.0f, cols, at);
   const Share row = share_of(cols);
   // At 16 columns a lane registers do not hold four sums (8 x 256 of 16384: 349 us,
-  // spilled, against 171): the branch's two lie in LDS, each lane's in its own place.
+  // spilled, against 168): the branch's two lie in LDS, each lane's in its own place.
   constexpr bool kLow = NC * V > 8;
   constexpr int S = kLow ? 2 : 4;
   using Low = float __attribute__((ext_vector_type(4)));

@@ -1,6 +1,6 @@
-// rows.hpp -- what the row-wise layer operators (norm.hip, join.hip) share: how
-// a row lies over the lanes of one wave or of several, parameter vectors, and
-// taking the mean off.
+// rows.hpp -- a layer norm's rows (norm.hip): how they lie over the lanes of one
+// wave or of several, parameter vectors, whose pieces join.hip reads too (Four),
+// and taking the mean off.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -14,7 +14,7 @@ namespace {
 
 // A lane's columns: chunk c holds kVec consecutive columns from
 // (c * W * 64 + thread) * kVec, W the waves that share a row (a power of two; a
-// block may hold several rows, each with W waves of its own).
+// block holds four rows of one wave or one row).
 template <typename T, int W>
 __device__ __forceinline__ int32_t chunk_col(int c) {
   const int32_t t = (int32_t)threadIdx.x & (W * 64 - 1);
