@@ -143,6 +143,10 @@ int oba_residual_norm_backward(int32_t n, int64_t rows, int64_t cols, int dtype,
       (!gate && dgate))
     return OBA_EINVAL;
   for (void* g : grads) OBA_TRY(check_opt(g, size_of(g_dtype)));
+  // read for the parameters' gradients also where there are no rows
+  OBA_TRY(check_opt(gamma_b, 4));
+  OBA_TRY(check_opt(beta_b, 4));
+  OBA_TRY(check_opt(gate, 4));
   if (rows > 0) {
     if ((!gamma && (dz || q || e || rstd)) || (!gamma_b && rstd_b) || (!gamma && !dr))
       return OBA_EINVAL;
@@ -157,12 +161,7 @@ int oba_residual_norm_backward(int32_t n, int64_t rows, int64_t cols, int dtype,
     OBA_TRY(check_opt(dr, 16));
     OBA_TRY(check_ptr(dx, 16));
     if (qb || eb) OBA_TRY(check_kept(qb, eb));
-    if (gamma_b) {
-      OBA_TRY(check_ptr(gamma_b, 4));
-      OBA_TRY(check_ptr(rstd_b, 4));
-    }
-    OBA_TRY(check_opt(beta_b, 4));
-    OBA_TRY(check_opt(gate, 4));
+    if (gamma_b) OBA_TRY(check_ptr(rstd_b, 4));
     OBA_TRY(check_rng(d));
     OBA_TRY(check_opt(db, 16));
     if (any) OBA_TRY(check_ws(ws, ws_bytes, join_ws(n, rows, cols)));
