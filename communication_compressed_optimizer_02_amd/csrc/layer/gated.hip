@@ -332,7 +332,7 @@ __global__ __launch_bounds__(WA* WB * 64, 3) void k_gated(Gated a, Tiles t) {
 // Bound by the products, and between them by the memory: all CUs end a tile at one
 // time, so its stores (and back its loads) run at 4.4 TB/s with the matrix cores
 // idle.  16384 x 1024 -> 2 x 4096 bfloat16: nothing kept 231 us, all kept (340 MB)
-// 289 to 312; the hidden gradient 120 us of products, 205 to 217 with its 400 MB.
+// 283 to 312; the hidden gradient 120 us of products, 203 to 217 with its 400 MB.
 // 8192 x 4096 -> 2 x 4096, nothing kept, 414 us, 1.33 PFLOP/s, the matrix cores busy
 // for 70 % of the cycles.  Two blocks of half the tile to a CU, one's epilogue under
 // the other's products, read half as much again from L2 and lost: 360 and 227.
